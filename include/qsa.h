@@ -60,6 +60,8 @@ extern "C" {
 #define QSA_MAX_CELLS (1 << 24)
 #define QSA_MAX_ROWS 65535  /* query rows of one prefill, qsa_topk or qsa_attn call */
 #define QSA_PART_STRIDE (2 + QSA_D) /* floats per partial: m, l, o[256] */
+#define QSA_MAX_HEADS 1024          /* query or KV heads of a batched call */
+#define QSA_MAX_PACKED (1 << 24)    /* packed rows of a batched call */
 
 enum {
   QSA_OK = 0,
@@ -70,6 +72,9 @@ enum {
 };
 
 enum { QSA_MODE_DECODE = 0, QSA_MODE_PREFILL = 1 };
+
+/* Types of the rows that the batched calls take. */
+enum { QSA_F32 = 0, QSA_F16 = 1, QSA_BF16 = 2 };
 
 /*
  * The cell cache ("random int8 KV, fp16 scales": "opus r20 track A ...",
@@ -264,6 +269,98 @@ int qsa_merge(const float* part, int rows, int nsplit, const float* gate, float*
 #define QSA_STATIC_SCRATCH_BYTES 1183744
 int qsa_topk_static(const float* scores, int64_t ld, int rows, int vis0, int top_k, int32_t* ids,
                     void* stream);
+
+/* ---- batches of sequences: a paged cache, its decode attention, packed prompts ----
+ *
+ * The calls above serve one sequence in one contiguous cache.  These serve many: each
+ * sequence's cells lie in pages of a shared pool, and the rows of all sequences come packed
+ * one after the other.  They have the step's dense form (every visible cell is attended, as
+ * in the calls above when a token sees at most top_k cells) and its head dim of 256; the head
+ * counts are free (query head h uses KV head h / (hq / hkv)).  Rows are fp32, fp16 or bf16
+ * ("dtype": one type for a call's inputs and outputs), each row's heads contiguous, rows `ld`
+ * elements apart (ld * element size a multiple of 16 bytes), so a slice of a wider projection
+ * row needs no copy.
+ */
+
+/*
+ * The pool: cell i of page p holds, for KV head g, what a qsa_cache cell holds:
+ * k, v [pages][page_cells][hkv][256] int8 and ks, vs [pages][page_cells][hkv][8] fp16.
+ * Any page_cells >= 1; pages * page_cells <= 2^30.
+ */
+typedef struct qsa_paged_cache {
+  int8_t* k;
+  int8_t* v;
+  uint16_t* ks;
+  uint16_t* vs;
+  int32_t pages;
+  int32_t page_cells;
+  int32_t hkv;
+} qsa_paged_cache;
+
+/*
+ * The sequences of a call, all in device memory (so a captured call follows them):
+ *   table   [nseq][table_ld] pages: position p of sequence s is cell p % page_cells of page
+ *           table[s][p / page_cells].  Entries past a sequence's end are not read; an entry
+ *           outside [0, pages) has no cells (nothing is written, attended or read there).
+ *   kv_len  [nseq] cells of each sequence, this call's own tokens included
+ *   cu_q    [nseq + 1] ascending, cu_q[0] = 0: sequence s has the packed rows cu_q[s] ..
+ *           cu_q[s+1] - 1, its LAST positions: row j of n is position kv_len - n + j.
+ *           NULL: one row per sequence.
+ * Sequences may be empty (no rows, or no cells).  Packed rows at or past cu_q[nseq] belong to
+ * no sequence: they are not read, and outputs there are left as they were.
+ * 1 <= nseq <= QSA_MAX_ROWS, 0 <= rows <= QSA_MAX_PACKED packed rows in the arrays.
+ */
+typedef struct qsa_batch {
+  const int32_t* table;
+  const int32_t* kv_len;
+  const int32_t* cu_q;
+  int32_t nseq;
+  int32_t table_ld;
+} qsa_batch;
+
+/*
+ * Quantise packed K/V rows [rows][hkv][256] of any dtype into their cells, per group of 32
+ * values (widened to fp32):
+ *   s = fp16_rn(max|x| * fp32(1 / 127)), saturated at 65504;
+ *   code = clamp(rint(x / s), -127, 127) (half to even), all 0 when s == 0;
+ * as qsa_cache_write, whose quotient max|x| / 127 gives a scale one fp16 step away in about
+ * three groups of a million.  Rows whose position is negative or has no page are skipped.
+ * Two rows must not share a cell.
+ */
+int qsa_paged_write(const qsa_paged_cache* cache, const qsa_batch* batch, int rows, int dtype,
+                    const void* k, int64_t ldk, const void* v, int64_t ldv, void* stream);
+
+/*
+ * The reverse: packed rows [rows][hkv][256] of code * scale, rounded once to dtype.  With
+ * cu_q[s+1] - cu_q[s] = kv_len[s] whole sequences are read back (for instance as the k and v
+ * of qsa_prompt_attn, when a prompt continues a cached prefix).  Rows whose position is
+ * negative or has no page read as 0.
+ */
+int qsa_paged_read(const qsa_paged_cache* cache, const qsa_batch* batch, int rows, int dtype,
+                   void* k, int64_t ldk, void* v, int64_t ldv, void* stream);
+
+/* Workspace bytes of qsa_paged_decode (0 for sizes that it refuses). */
+size_t qsa_paged_decode_workspace_bytes(int nseq, int hq, int hkv, int max_q, int max_len);
+
+/*
+ * Attention of each sequence's newest tokens over its cells, split over the cells and joined
+ * by log-sum-exp.  Row j of a sequence's n sees positions [0, kv_len - n + 1 + j):
+ *   out[r][h] = softmax_c(scale * q[r][h] . K[c]) . V[c]   (* sigmoid(gate[r][h]))
+ * and is 0 when it sees none.  The cells must have been written before (qsa_paged_write on
+ * the same stream).
+ *   q, out   [rows][hq][256] of dtype, ldq / ldo elements apart; gate likewise or NULL
+ *   max_q    no sequence has more rows (1 .. 8); rows past max_q of a sequence are not computed
+ *   max_len  no sequence is longer; positions at or past max_len are not attended
+ *   ws       at least qsa_paged_decode_workspace_bytes(...) bytes, one call at a time
+ * Requires max_q * hq / hkv <= 96.  The result does not depend on how the cells are split
+ * beyond rounding and is the same in every run.  fp16 / bf16: q and the weights enter the
+ * tensor cores as fp16, V as fp16(code * scale); fp32: each as a pair of fp16 (22 bits).  So
+ * |q| and |V| up to 65504 are held; accumulation and the softmax are fp32.
+ */
+int qsa_paged_decode(const qsa_paged_cache* cache, const qsa_batch* batch, int rows, int max_q,
+                     int max_len, int dtype, int hq, const void* q, int64_t ldq, const void* gate,
+                     int64_t ldg, float scale, void* ws, size_t ws_bytes, void* out, int64_t ldo,
+                     void* stream);
 
 /*
  * Device-side failure report.  Kernels that wait on an mbarrier (the prefill

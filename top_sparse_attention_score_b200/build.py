@@ -23,7 +23,7 @@ FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std
 
 def sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")) + glob.glob(os.path.join(CSRC, "*.cuh"))
-                  + [os.path.join(INCLUDE, "qsa.h")])
+                  + glob.glob(os.path.join(CSRC, "*.h")) + [os.path.join(INCLUDE, "qsa.h")])
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -32,8 +32,9 @@ def build(force: bool = False, verbose: bool = False) -> str:
         newest = max(os.path.getmtime(p) for p in sources())
         if os.path.getmtime(LIB) >= newest:
             return LIB
-    cmd = [NVCC, *FLAGS, *(["-Xptxas", "-v"] if verbose else []),
-           os.path.join(CSRC, "qsa_api.cu"), "-o", LIB + ".tmp"]
+    # --threads compiles the translation units side by side
+    cmd = [NVCC, *FLAGS, *(["-Xptxas", "-v"] if verbose else []), "--threads", "0",
+           *sorted(glob.glob(os.path.join(CSRC, "*.cu"))), "-o", LIB + ".tmp"]
     subprocess.run(cmd, check=True)
     os.replace(LIB + ".tmp", LIB)
     return LIB

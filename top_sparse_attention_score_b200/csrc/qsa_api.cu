@@ -18,6 +18,7 @@
 #include "qsa_attn.cuh"
 #include "qsa_cache_write.cuh"
 #include "qsa_common.cuh"
+#include "qsa_host.h"
 #include "qsa_index_score.cuh"
 #include "qsa_merge.cuh"
 #include "qsa_prefill_select.cuh"
@@ -29,10 +30,28 @@
 // QSA_ERR_TIMEOUT here (read and cleared by qsa_device_status).
 static __device__ uint32_t g_device_status;
 
+using namespace qsa::host;
+
 namespace {
 
 thread_local std::string g_error;
 std::atomic<uint64_t> g_launches{0};
+
+// Per-kernel timing of this thread's calls (qsa_trace_begin / qsa_trace_end): an event
+// on the traced stream before the first launch and after every launch.
+struct Trace {
+  bool on = false;
+  cudaStream_t stream = nullptr;
+  std::vector<cudaEvent_t> ev;     // ev[0]: the start; ev[i + 1]: after launch i
+  std::vector<const char*> names;  // kernel of launch i
+  int n = 0;
+};
+thread_local Trace g_trace;
+
+}  // namespace
+
+namespace qsa {
+namespace host {
 
 int fail(int code, const char* fmt, ...) {
   char buf[512];
@@ -48,17 +67,6 @@ int ok() {
   g_error.clear();
   return QSA_OK;
 }
-
-// Per-kernel timing of this thread's calls (qsa_trace_begin / qsa_trace_end): an event
-// on the traced stream before the first launch and after every launch.
-struct Trace {
-  bool on = false;
-  cudaStream_t stream = nullptr;
-  std::vector<cudaEvent_t> ev;     // ev[0]: the start; ev[i + 1]: after launch i
-  std::vector<const char*> names;  // kernel of launch i
-  int n = 0;
-};
-thread_local Trace g_trace;
 
 // Count a launch and turn the error its launch call returned into QSA_ERR_CUDA.
 // Only a failed launch clears the runtime's last-error state (which it set): an
@@ -77,28 +85,10 @@ int launched(const char* what, cudaError_t e) {
   return QSA_OK;
 }
 
-// Launch with programmatic stream serialisation: the kernel may be scheduled
-// while its predecessor on the stream drains; every kernel here waits on
-// griddepcontrol.wait before touching memory its predecessors use.
-template <typename... KArgs, typename... Args>
-cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
-                       Args&&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = block;
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
-}
+}  // namespace host
+}  // namespace qsa
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
+namespace {
 
 int check_cache(const qsa_cache* c) {
   if (!c) return fail(QSA_ERR_ARG, "cache is NULL");
@@ -117,6 +107,11 @@ uint32_t* g_status_addr[64] = {};
 bool g_wide_cluster[64] = {};  // a 16-CTA selection cluster can be scheduled on this device
 
 bool wide_cluster_fits();
+
+}  // namespace
+
+namespace qsa {
+namespace host {
 
 // Opt the kernels that need it into large dynamic shared memory and read the
 // SM count, once per device.
@@ -181,6 +176,11 @@ int sm_count() {
   cudaGetDevice(&dev);
   return g_sm_count[dev & 63] > 0 ? g_sm_count[dev & 63] : 148;
 }
+
+}  // namespace host
+}  // namespace qsa
+
+namespace {
 
 // ---- workspace plan -------------------------------------------------------
 
@@ -297,6 +297,11 @@ StepPlan plan_step(int rows, int ncells, int vmax, int top_k, int nsplit) {
 PFN_cuTensorMapEncodeTiled_v12000 g_encode_tiled = nullptr;
 std::mutex g_encode_mu;
 
+}  // namespace
+
+namespace qsa {
+namespace host {
+
 int tensor_map_encoder(PFN_cuTensorMapEncodeTiled_v12000* out) {
   std::lock_guard<std::mutex> lock(g_encode_mu);
   if (!g_encode_tiled) {
@@ -310,6 +315,11 @@ int tensor_map_encoder(PFN_cuTensorMapEncodeTiled_v12000* out) {
   *out = g_encode_tiled;
   return QSA_OK;
 }
+
+}  // namespace host
+}  // namespace qsa
+
+namespace {
 
 // Scores of `rows` > 8 rows: the tcgen05 GEMM, keys and queries fed by TMA.
 int launch_score_gemm(const qsa_cache* c, int rows, int ncells, const uint16_t* iq, const float* iw,

@@ -1,0 +1,254 @@
+// qsa_paged.cu -- the C ABI of batched serving (include/qsa.h): the paged int8 cache, its
+// decode attention and the packed prompt attention.  Argument checks, workspace planning and
+// launches; the computation is in the kernels of the qsa_paged_*.cuh and qsa_prompt_attn.cuh files.
+#include <algorithm>
+#include <atomic>
+
+#include "qsa_host.h"
+#include "qsa_paged_cache.cuh"
+#include "qsa_paged_decode.cuh"
+
+using namespace qsa::host;
+
+namespace {
+
+int elem_size(int dtype) { return dtype == QSA_F32 ? 4 : 2; }
+
+int check_dtype(int dtype) {
+  if (dtype != QSA_F32 && dtype != QSA_F16 && dtype != QSA_BF16)
+    return fail(QSA_ERR_ARG, "dtype = %d is none of QSA_F32, QSA_F16, QSA_BF16", dtype);
+  return QSA_OK;
+}
+
+// A packed array of rows of `heads` heads x 256: 16-byte aligned rows that do not overlap.
+int check_rows(const char* name, const void* p, int64_t ld, int heads, int dtype) {
+  if (!p) return fail(QSA_ERR_ARG, "%s must not be NULL", name);
+  const int64_t need = static_cast<int64_t>(heads) * QSA_D;
+  if (ld < need || (ld * elem_size(dtype)) % 16 || ld > (static_cast<int64_t>(1) << 31))
+    return fail(QSA_ERR_ARG, "%s row stride %lld must be >= %lld and a multiple of 16 bytes", name,
+                static_cast<long long>(ld), static_cast<long long>(need));
+  if (!aligned16(p)) return fail(QSA_ERR_ARG, "%s must be 16-byte aligned", name);
+  return QSA_OK;
+}
+
+int check_paged(const qsa_paged_cache* c, const qsa_batch* b, int rows) {
+  if (!c) return fail(QSA_ERR_ARG, "cache is NULL");
+  if (!c->k || !c->v || !c->ks || !c->vs) return fail(QSA_ERR_ARG, "cache has a NULL array");
+  if (!aligned16(c->k) || !aligned16(c->v) || !aligned16(c->ks) || !aligned16(c->vs))
+    return fail(QSA_ERR_ARG, "cache arrays must be 16-byte aligned");
+  if (c->hkv < 1 || c->hkv > QSA_MAX_HEADS) return fail(QSA_ERR_ARG, "cache hkv = %d out of [1, %d]", c->hkv, QSA_MAX_HEADS);
+  if (c->pages < 1 || c->page_cells < 1 ||
+      static_cast<int64_t>(c->pages) * c->page_cells > (static_cast<int64_t>(1) << 30))
+    return fail(QSA_ERR_ARG, "cache of %d pages of %d cells: both at least 1, at most 2^30 cells", c->pages,
+                c->page_cells);
+  if (!b) return fail(QSA_ERR_ARG, "batch is NULL");
+  if (!b->table || !b->kv_len) return fail(QSA_ERR_ARG, "batch has a NULL array");
+  if (b->nseq < 1 || b->nseq > QSA_MAX_ROWS || b->table_ld < 1)
+    return fail(QSA_ERR_ARG, "batch nseq = %d out of [1, %d] or table_ld = %d below 1", b->nseq, QSA_MAX_ROWS, b->table_ld);
+  if (rows < 0 || rows > QSA_MAX_PACKED) return fail(QSA_ERR_ARG, "rows = %d out of [0, %d]", rows, QSA_MAX_PACKED);
+  return QSA_OK;
+}
+
+qsa::PagedBatch device_batch(const qsa_paged_cache* c, const qsa_batch* b) {
+  qsa::PagedBatch r;
+  r.table = b->table;
+  r.kv_len = b->kv_len;
+  r.cu = b->cu_q;
+  r.nseq = b->nseq;
+  r.table_ld = b->table_ld;
+  r.page_cells = c->page_cells;
+  r.pages = c->pages;
+  return r;
+}
+
+qsa::PagedCells device_cells(const qsa_paged_cache* c) {
+  qsa::PagedCells r;
+  r.k = c->k;
+  r.v = c->v;
+  r.ks = reinterpret_cast<__half*>(c->ks);
+  r.vs = reinterpret_cast<__half*>(c->vs);
+  r.hkv = c->hkv;
+  return r;
+}
+
+template <typename T>
+cudaError_t launch_write(const qsa::PagedBatch& b, const qsa::PagedCells& c, int rows, const void* k, const void* v,
+                         int64_t ldk, int64_t ldv, cudaStream_t s) {
+  return launch_pdl(qsa::paged_write_kernel<T>, dim3((rows + qsa::kPagedWarps - 1) / qsa::kPagedWarps),
+                    dim3(32 * qsa::kPagedWarps), 0, s, b, c, rows, static_cast<const T*>(k), static_cast<const T*>(v),
+                    ldk, ldv);
+}
+
+template <typename T>
+cudaError_t launch_read(const qsa::PagedBatch& b, const qsa::PagedCells& c, int rows, void* k, void* v, int64_t ldk,
+                        int64_t ldv, cudaStream_t s) {
+  return launch_pdl(qsa::paged_read_kernel<T>, dim3((rows + qsa::kPagedWarps - 1) / qsa::kPagedWarps),
+                    dim3(32 * qsa::kPagedWarps), 0, s, b, c, rows, static_cast<T*>(k), static_cast<T*>(v), ldk, ldv);
+}
+
+// ---- decode plan
+
+// Kernel shape for a call's row tiles: the tiles of 16 query rows (warps of a group) and the
+// groups of a CTA; two CTAs per SM where registers and shared memory allow.
+struct DecodePlan {
+  int mt, groups, ctas_per_sm, prows, block_cells;
+  int64_t blocks;  // upper bound of the flat list
+  int grid;
+  size_t part_o, part_ml, unit, total;
+};
+
+DecodePlan plan_decode(int nseq, int hkv, int group, int max_q, int64_t max_len, bool split, int sms) {
+  DecodePlan p;
+  p.mt = (max_q * group + 15) / 16;
+  p.groups = p.mt == 1 ? 4 : p.mt == 2 ? 2 : 1;
+  p.ctas_per_sm = p.mt <= 3 || (p.mt == 4 && !split) ? 2 : 1;
+  p.prows = 16 * p.mt;
+  p.block_cells = 16 * p.groups;
+  p.blocks = static_cast<int64_t>(nseq) * hkv * ((max_len + p.block_cells - 1) / p.block_cells);
+  p.grid = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(p.blocks, static_cast<int64_t>(sms) * p.ctas_per_sm)));
+  p.part_o = 0;
+  p.part_ml = align_up(p.part_o + static_cast<size_t>(2) * p.grid * p.prows * QSA_D * 4, 256);
+  p.unit = align_up(p.part_ml + static_cast<size_t>(2) * p.grid * p.prows * 8, 256);
+  p.total = align_up(p.unit + static_cast<size_t>(nseq) * hkv * 8, 256);
+  return p;
+}
+
+constexpr int kPlanSms = 160;  // the workspace is planned for at most this many SMs
+
+int check_decode_sizes(int nseq, int hq, int hkv, int max_q, int64_t max_len) {
+  if (hkv < 1 || hkv > QSA_MAX_HEADS || hq < 1 || hq > QSA_MAX_HEADS || hq % hkv)
+    return fail(QSA_ERR_ARG, "hq = %d must be a multiple of hkv = %d, both in [1, %d]", hq, hkv, QSA_MAX_HEADS);
+  if (nseq < 1 || nseq > QSA_MAX_ROWS) return fail(QSA_ERR_ARG, "nseq = %d out of [1, %d]", nseq, QSA_MAX_ROWS);
+  if (max_q < 1 || max_q > QSA_MAX_DECODE) return fail(QSA_ERR_ARG, "max_q = %d out of [1, %d]", max_q, QSA_MAX_DECODE);
+  if (max_q * (hq / hkv) > qsa::kPdMaxRows)
+    return fail(QSA_ERR_ARG, "max_q = %d tokens x %d heads per KV head above %d rows", max_q, hq / hkv, qsa::kPdMaxRows);
+  if (max_len < 1 || static_cast<int64_t>(nseq) * hkv * ((max_len + 15) / 16) >= (static_cast<int64_t>(1) << 30))
+    return fail(QSA_ERR_ARG, "max_len = %lld of %d sequences x %d KV heads out of range", static_cast<long long>(max_len), nseq, hkv);
+  return QSA_OK;
+}
+
+template <typename T, int MT, int C, int STAGES, int MINB>
+cudaError_t launch_decode_shape(const qsa::PdArgs& a, int grid, cudaStream_t s) {
+  using Smem = qsa::PdSmem<MT, C, STAGES, sizeof(T) == 4>;
+  auto kernel = qsa::paged_decode_kernel<T, MT, C, STAGES, MINB>;
+  // Opt in to the dynamic shared memory once per device.
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (!(done.load(std::memory_order_relaxed) & bit)) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem::kBytes);
+    if (e != cudaSuccess) return e;
+    done.fetch_or(bit, std::memory_order_relaxed);
+  }
+  return launch_pdl(kernel, dim3(grid), dim3(32 * MT * C), Smem::kBytes, s, a);
+}
+
+template <typename T>
+int launch_decode(const qsa::PdArgs& a, const DecodePlan& p, int hq, cudaStream_t s) {
+  constexpr bool split = sizeof(T) == 4;
+  cudaError_t e = cudaSuccess;
+  switch (p.mt) {
+    case 1: e = launch_decode_shape<T, 1, 4, split ? 2 : 3, 2>(a, p.grid, s); break;
+    case 2: e = launch_decode_shape<T, 2, 2, 4, 2>(a, p.grid, s); break;
+    case 3: e = launch_decode_shape<T, 3, 1, 5, 2>(a, p.grid, s); break;
+    case 4: e = launch_decode_shape<T, 4, 1, 6, split ? 1 : 2>(a, p.grid, s); break;
+    case 5: e = launch_decode_shape<T, 5, 1, 8, 1>(a, p.grid, s); break;
+    default: e = launch_decode_shape<T, 6, 1, 8, 1>(a, p.grid, s); break;
+  }
+  int r = launched("paged_decode_kernel", e);
+  if (r) return r;
+  return launched("paged_join_kernel", launch_pdl(qsa::paged_join_kernel<T>, dim3(a.rows, hq), dim3(32 * qsa::kPjWarps), 0, s, a));
+}
+
+}  // namespace
+
+extern "C" {
+
+int qsa_paged_write(const qsa_paged_cache* cache, const qsa_batch* batch, int rows, int dtype, const void* k,
+                    int64_t ldk, const void* v, int64_t ldv, void* stream) {
+  int r = check_paged(cache, batch, rows);
+  if (r) return r;
+  if ((r = check_dtype(dtype))) return r;
+  if (rows == 0) return ok();
+  if ((r = check_rows("k", k, ldk, cache->hkv, dtype)) || (r = check_rows("v", v, ldv, cache->hkv, dtype))) return r;
+  const qsa::PagedBatch b = device_batch(cache, batch);
+  const qsa::PagedCells c = device_cells(cache);
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = dtype == QSA_F32   ? launch_write<float>(b, c, rows, k, v, ldk, ldv, s)
+                        : dtype == QSA_F16 ? launch_write<__half>(b, c, rows, k, v, ldk, ldv, s)
+                                           : launch_write<__nv_bfloat16>(b, c, rows, k, v, ldk, ldv, s);
+  if ((r = launched("paged_write_kernel", e))) return r;
+  return ok();
+}
+
+int qsa_paged_read(const qsa_paged_cache* cache, const qsa_batch* batch, int rows, int dtype, void* k, int64_t ldk,
+                   void* v, int64_t ldv, void* stream) {
+  int r = check_paged(cache, batch, rows);
+  if (r) return r;
+  if ((r = check_dtype(dtype))) return r;
+  if (rows == 0) return ok();
+  if ((r = check_rows("k", k, ldk, cache->hkv, dtype)) || (r = check_rows("v", v, ldv, cache->hkv, dtype))) return r;
+  const qsa::PagedBatch b = device_batch(cache, batch);
+  const qsa::PagedCells c = device_cells(cache);
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = dtype == QSA_F32   ? launch_read<float>(b, c, rows, k, v, ldk, ldv, s)
+                        : dtype == QSA_F16 ? launch_read<__half>(b, c, rows, k, v, ldk, ldv, s)
+                                           : launch_read<__nv_bfloat16>(b, c, rows, k, v, ldk, ldv, s);
+  if ((r = launched("paged_read_kernel", e))) return r;
+  return ok();
+}
+
+size_t qsa_paged_decode_workspace_bytes(int nseq, int hq, int hkv, int max_q, int max_len) {
+  if (check_decode_sizes(nseq, hq, hkv, max_q, max_len)) return 0;
+  return std::max(plan_decode(nseq, hkv, hq / hkv, max_q, max_len, false, kPlanSms).total,
+                  plan_decode(nseq, hkv, hq / hkv, max_q, max_len, true, kPlanSms).total);
+}
+
+int qsa_paged_decode(const qsa_paged_cache* cache, const qsa_batch* batch, int rows, int max_q, int max_len, int dtype,
+                     int hq, const void* q, int64_t ldq, const void* gate, int64_t ldg, float scale, void* ws,
+                     size_t ws_bytes, void* out, int64_t ldo, void* stream) {
+  int r = check_paged(cache, batch, rows);
+  if (r) return r;
+  if ((r = check_dtype(dtype))) return r;
+  if ((r = check_decode_sizes(batch->nseq, hq, cache->hkv, max_q, max_len))) return r;
+  if (rows == 0) return ok();
+  if ((r = check_rows("q", q, ldq, hq, dtype)) || (r = check_rows("out", out, ldo, hq, dtype)) ||
+      (gate && (r = check_rows("gate", gate, ldg, hq, dtype))))
+    return r;
+  if (!ws) return fail(QSA_ERR_WORKSPACE, "workspace is NULL");
+  if (!aligned16(ws)) return fail(QSA_ERR_ARG, "ws must be 16-byte aligned");
+  const bool split = dtype == QSA_F32;
+  if ((r = prepare_device())) return r;
+  const int group = hq / cache->hkv;
+  const DecodePlan p = plan_decode(batch->nseq, cache->hkv, group, max_q, max_len, split, std::min(sm_count(), kPlanSms));
+  if (ws_bytes < p.total) return fail(QSA_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", ws_bytes, p.total);
+  qsa::PdArgs a;
+  a.b = device_batch(cache, batch);
+  a.c = device_cells(cache);
+  a.q = q;
+  a.gate = gate;
+  a.out = out;
+  a.ldq = ldq;
+  a.ldg = ldg;
+  a.ldo = ldo;
+  a.rows = rows;
+  a.max_q = max_q;
+  a.max_len = max_len;
+  a.group = group;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  char* base = static_cast<char*>(ws);
+  a.part_o = reinterpret_cast<float*>(base + p.part_o);
+  a.part_ml = reinterpret_cast<float2*>(base + p.part_ml);
+  a.unit = reinterpret_cast<int2*>(base + p.unit);
+  a.prows = p.prows;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  r = dtype == QSA_F32   ? launch_decode<float>(a, p, hq, s)
+      : dtype == QSA_F16 ? launch_decode<__half>(a, p, hq, s)
+                         : launch_decode<__nv_bfloat16>(a, p, hq, s);
+  if (r) return r;
+  return ok();
+}
+
+}  // extern "C"

@@ -1,0 +1,248 @@
+// qsa_paged_cache.cuh -- quantise packed K/V rows into a paged int8 cache, and read them back.
+//
+// Write, per group of 32 values: s = fp16_rn(max|x| * fp32(1 / 127)) saturated at 65504,
+// code = clamp(rint(x / s), -127, 127), all 0 when s == 0, each step rounded in IEEE fp32
+// (fp16 and bf16 rows are widened exactly first).  qsa_cache_write divides the maximum by 127;
+// the product differs from the quotient by an fp32 step at most, so three scales in a million
+// are one fp16 step away from that call's and the codes of the others are the same.
+// Read: code * s, exact in fp32 (7 + 11 bits), rounded once to the output type.
+//
+// Both only move data: a row of one KV head is 256 values in and 256 codes + 16 bytes of
+// scales out (or back), so HBM bandwidth bounds long calls and latency short ones.  One warp
+// takes a whole packed row (all KV heads, K and V), so the search for the row's sequence and
+// the page lookup are paid once, and its 2 * hkv head rows go through four at a time with
+// all their loads issued first.  A lane holds 8 consecutive values: a group of 32 is four
+// neighbouring lanes (two shuffles for its maximum), and every access is 8 to 16 bytes a lane.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "qsa_common.cuh"
+
+namespace qsa {
+
+// The batch as kernels take it (qsa_batch; cu NULL: one row per sequence).
+struct PagedBatch {
+  const int* table;   // [nseq][table_ld]
+  const int* kv_len;  // [nseq]
+  const int* cu;      // [nseq + 1] or NULL
+  int nseq;
+  int table_ld;
+  int page_cells;
+  int pages;
+};
+
+struct PagedCells {
+  int8_t* k;
+  int8_t* v;
+  __half* ks;
+  __half* vs;
+  int hkv;
+};
+
+__device__ __forceinline__ int batch_row0(const PagedBatch& b, int s) { return b.cu ? __ldg(b.cu + s) : s; }
+
+// Sequence of packed row r (the s with cu[s] <= r < cu[s + 1]), -1 when no sequence has it.
+// 32-ary search by the warp: one load and one ballot per factor of 32 sequences.
+__device__ __forceinline__ int batch_find(const PagedBatch& b, int r, int lane) {
+  if (!b.cu) return r < b.nseq ? r : -1;
+  int lo = 0, n = b.nseq;  // the answer is the number of s with cu[s + 1] <= r, within [lo, lo + n]
+  while (n > 0) {
+    const int step = (n + 31) >> 5;
+    const int i = lo + (lane + 1) * step - 1;  // last sequence of this lane's block
+    const bool below = i < lo + n && __ldg(b.cu + i + 1) <= r;
+    const int full = __popc(__ballot_sync(0xffffffffu, below));
+    if (step == 1) {
+      lo += full;
+      break;
+    }
+    n = min(step, n - full * step);
+    lo += full * step;
+  }
+  return lo < b.nseq && r >= __ldg(b.cu) ? lo : -1;
+}
+
+// Cell of position p of sequence s; -1 when the position, its table entry or its page does not exist.
+__device__ __forceinline__ int batch_cell(const PagedBatch& b, int s, int p) {
+  if (p < 0) return -1;
+  const int j = static_cast<int>(static_cast<unsigned>(p) / static_cast<unsigned>(b.page_cells));
+  if (j >= b.table_ld) return -1;
+  const int page = __ldg(b.table + static_cast<size_t>(s) * b.table_ld + j);
+  if (page < 0 || page >= b.pages) return -1;
+  return page * b.page_cells + (p - j * b.page_cells);
+}
+
+// Position of packed row r of sequence s: the rows are the sequence's last positions.
+__device__ __forceinline__ int batch_position(const PagedBatch& b, int s, int r) {
+  const int end = b.cu ? __ldg(b.cu + s + 1) : s + 1;
+  return __ldg(b.kv_len + s) - end + r;
+}
+
+// ---- 8 consecutive values of a row in a lane
+
+template <typename T>
+struct Row8;
+
+template <>
+struct Row8<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = __ldg(reinterpret_cast<const float4*>(p));
+    b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+  }
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+  }
+  static __device__ __forceinline__ void store(float* p, const float (&x)[8]) {
+    reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+  }
+};
+
+template <>
+struct Row8<__half> {
+  uint4 a;
+  __device__ __forceinline__ void load(const __half* p) { a = __ldg(reinterpret_cast<const uint4*>(p)); }
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+      x[2 * i] = f.x;
+      x[2 * i + 1] = f.y;
+    }
+  }
+  static __device__ __forceinline__ void store(__half* p, const float (&x)[8]) {
+    *reinterpret_cast<uint4*>(p) = make_uint4(pack_half2(x[0], x[1]), pack_half2(x[2], x[3]),
+                                              pack_half2(x[4], x[5]), pack_half2(x[6], x[7]));
+  }
+};
+
+__device__ __forceinline__ uint32_t pack_bf162(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+template <>
+struct Row8<__nv_bfloat16> {
+  uint4 a;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { a = __ldg(reinterpret_cast<const uint4*>(p)); }
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = __uint_as_float(w[i] << 16);
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+  static __device__ __forceinline__ void store(__nv_bfloat16* p, const float (&x)[8]) {
+    *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf162(x[0], x[1]), pack_bf162(x[2], x[3]),
+                                              pack_bf162(x[4], x[5]), pack_bf162(x[6], x[7]));
+  }
+};
+
+constexpr int kPagedWarps = 4;  // packed rows per CTA of the write and the read
+
+// Head row i of a packed row's 2 * hkv: K of head i for i < hkv, else V of head i - hkv.
+// grid: ceil(rows / 4); block: 128.
+template <typename T>
+__global__ void __launch_bounds__(32 * kPagedWarps) paged_write_kernel(PagedBatch b, PagedCells c, int rows,
+                                                                      const T* __restrict__ k,
+                                                                      const T* __restrict__ v, int64_t ldk,
+                                                                      int64_t ldv) {
+  const int lane = threadIdx.x & 31;
+  const int r = blockIdx.x * kPagedWarps + (threadIdx.x >> 5);
+  // No early launch of dependents: a dependent may read the cells before its own wait.
+  griddep_wait();
+  if (r >= rows) return;
+  const int s = batch_find(b, r, lane);
+  if (s < 0) return;
+  const int cell = batch_cell(b, s, batch_position(b, s, r));
+  if (cell < 0) return;
+  const int items = 2 * c.hkv;
+  for (int i0 = 0; i0 < items; i0 += 4) {
+    Row8<T> raw[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int i = i0 + u;
+      if (i < items) {
+        const T* src = i < c.hkv ? k + r * ldk + i * kD : v + r * ldv + (i - c.hkv) * kD;
+        raw[u].load(src + 8 * lane);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int i = i0 + u;
+      if (i >= items) break;
+      float x[8];
+      raw[u].get(x);
+      float amax = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(x[e]));
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+      __half sc = __float2half_rn(__fmul_rn(amax, 1.0f / 127.0f));
+      float sf = __half2float(sc);
+      if (!(sf <= 65504.0f)) {
+        sc = __ushort_as_half(0x7bff);
+        sf = 65504.0f;
+      }
+      uint32_t w[2] = {0u, 0u};
+      if (sf != 0.0f) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int code = max(-127, min(127, __float2int_rn(__fdiv_rn(x[e], sf))));
+          w[e >> 2] |= (static_cast<uint32_t>(code) & 0xffu) << (8 * (e & 3));
+        }
+      }
+      const size_t row = static_cast<size_t>(cell) * c.hkv + (i < c.hkv ? i : i - c.hkv);
+      *reinterpret_cast<uint2*>((i < c.hkv ? c.k : c.v) + row * kD + 8 * lane) = make_uint2(w[0], w[1]);
+      if ((lane & 3) == 0) (i < c.hkv ? c.ks : c.vs)[row * kNG + (lane >> 2)] = sc;
+    }
+  }
+}
+
+// grid: ceil(rows / 4); block: 128.  A row whose position or page does not exist reads as 0.
+template <typename T>
+__global__ void __launch_bounds__(32 * kPagedWarps) paged_read_kernel(PagedBatch b, PagedCells c, int rows,
+                                                                     T* __restrict__ k, T* __restrict__ v,
+                                                                     int64_t ldk, int64_t ldv) {
+  const int lane = threadIdx.x & 31;
+  const int r = blockIdx.x * kPagedWarps + (threadIdx.x >> 5);
+  griddep_wait();
+  if (r >= rows) return;
+  const int s = batch_find(b, r, lane);
+  if (s < 0) return;
+  const int cell = batch_cell(b, s, batch_position(b, s, r));
+  const int items = 2 * c.hkv;
+  for (int i0 = 0; i0 < items; i0 += 4) {
+    uint2 w[4];
+    float sc[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int i = i0 + u;
+      w[u] = make_uint2(0u, 0u);
+      sc[u] = 0.f;
+      if (i < items && cell >= 0) {
+        const size_t row = static_cast<size_t>(cell) * c.hkv + (i < c.hkv ? i : i - c.hkv);
+        w[u] = *reinterpret_cast<const uint2*>((i < c.hkv ? c.k : c.v) + row * kD + 8 * lane);
+        sc[u] = __half2float((i < c.hkv ? c.ks : c.vs)[row * kNG + (lane >> 2)]);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int i = i0 + u;
+      if (i >= items) break;
+      float x[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const uint32_t word = e < 4 ? w[u].x : w[u].y;
+        x[e] = static_cast<float>(static_cast<int8_t>((word >> (8 * (e & 3))) & 0xffu)) * sc[u];
+      }
+      T* dst = i < c.hkv ? k + r * ldk + i * kD : v + r * ldv + (i - c.hkv) * kD;
+      Row8<T>::store(dst + 8 * lane, x);
+    }
+  }
+}
+
+}  // namespace qsa

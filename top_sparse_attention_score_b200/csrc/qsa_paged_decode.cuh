@@ -1,0 +1,576 @@
+// qsa_paged_decode.cuh -- attention of a sequence's newest tokens over all its cells in a
+// paged int8 K/V cache, split over the cells and joined.
+//
+// Mathematics: s_c = scale * sum_g ks[c][g] * (sum_{d in g} q[d] code_k[c][d]), an online softmax
+// (running maximum m, sum l, unnormalised o), o += p_c * vs[c][g] * code_v[c][d]; pieces of a
+// sequence's cells join by log-sum-exp.  Statistics and accumulators are fp32.
+//
+// Bound: HBM.  A cell of one KV head is 544 bytes, 23 SM cycles of this GPU's measured copy
+// rate, and serves all query rows of that head (tokens x heads per KV head, at most 96).
+//
+//  * Work is one flat list of blocks (sequence, KV head, 16 C cells) cut into equal contiguous
+//    ranges, one per CTA: ragged lengths balance themselves and a CTA writes one partial per
+//    sequence and head it touches.  Where a range covers a whole (sequence, head) its CTA writes
+//    the final rows itself.  Only the first and the last unit of a range can be partial, so CTA c
+//    has two partial slots: 2c for a unit begun before it, 2c + 1 for one that goes on after it.
+//    No counter or atomic orders anything.
+//  * MT warps hold the MT tiles of 16 query rows, C groups of MT warps take 16-cell blocks in
+//    turn.  A warp keeps 16 x 256 of O in registers (128 of them), so no score or weight is
+//    exchanged between warps; the C groups' results join once per piece through shared memory.
+//  * Cells arrive by cp.async in a ring of 16-cell stages a group owns (only its MT warps wait
+//    for it).  Rows are 256 bytes without padding; 32-byte pairs of chunks are XOR-swizzled by
+//    the cell, so the fragment reads (8 bytes of 4 cells, 4 bytes of 4 cell pairs) hit all banks.
+//  * Codes become fp16 exactly (byte permute into 0x64xx, minus 1152) and feed mma.sync m16n8k16.
+//    fp16 / bf16 calls: q enters as fp16 (bf16 q of ordinary size is exact), V as fp16(code * vs) and the
+//    weights as fp16: two roundings of 2^-12 against an output rounded to 2^-12 or 2^-9.
+//    fp32 calls (kSplit): q, the weights and code * vs are each a sum of two fp16 values, hi + lo,
+//    and the products hi hi + hi lo + lo hi are kept, so what is lost is 2^-22.
+#pragma once
+
+#include "qsa_attn.cuh"
+#include "qsa_paged_cache.cuh"
+
+namespace qsa {
+
+constexpr int kPdMaxRows = 96;  // query rows of one sequence and KV head
+
+// Shared-memory stage: 16 cells of one KV head.
+struct __align__(16) PdStage {
+  int8_t k[16 * kD];
+  int8_t v[16 * kD];
+  __half ks[16 * kNG];
+  __half vs[16 * kNG];
+};
+static_assert(sizeof(PdStage) == 8704, "544 bytes a cell");
+
+struct PdArgs {
+  PagedBatch b;
+  PagedCells c;
+  const void* q;
+  const void* gate;
+  void* out;
+  int64_t ldq, ldg, ldo;
+  int rows;      // packed rows of q and out
+  int max_q;
+  int max_len;
+  int group;     // query heads per KV head
+  float scale_log2;
+  float* part_o;   // [slots][prows][256]
+  float2* part_ml; // [slots][prows]: maximum (log2 units), sum
+  int2* unit;      // [nseq * hkv]: first CTA and number of pieces
+  int prows;       // rows of a partial: MT * 16
+};
+
+// Rows and cells of sequence s as this call sees them.
+struct PdSeq {
+  int row0;  // first packed row
+  int n;     // its rows, at most max_q
+  int len;   // true length (visibility)
+  int cells; // cells to visit
+};
+
+__device__ __forceinline__ PdSeq pd_seq(const PdArgs& a, int s) {
+  PdSeq q;
+  q.row0 = batch_row0(a.b, s);
+  const int end = min(a.b.cu ? __ldg(a.b.cu + s + 1) : s + 1, a.rows);
+  q.n = q.row0 < 0 ? 0 : max(0, end - q.row0);
+  q.len = max(0, __ldg(a.b.kv_len + s));
+  const int64_t held = static_cast<int64_t>(a.b.table_ld) * a.b.page_cells;
+  q.cells = q.n > 0 ? static_cast<int>(min(static_cast<int64_t>(min(q.len, a.max_len)), held)) : 0;
+  return q;
+}
+
+// Cells that row j of the sequence sees (its last visible position + 1).
+__device__ __forceinline__ int pd_visible(const PdSeq& q, int j) { return q.len - q.n + 1 + j; }
+
+template <typename T>
+__device__ __forceinline__ float pd_to_float(T x);
+template <>
+__device__ __forceinline__ float pd_to_float(float x) { return x; }
+template <>
+__device__ __forceinline__ float pd_to_float(__half x) { return __half2float(x); }
+template <>
+__device__ __forceinline__ float pd_to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
+
+// x = hi + lo with both in fp16 (lo holds the next 11 bits).
+__device__ __forceinline__ void pd_split2(float x, float y, uint32_t& hi, uint32_t& lo) {
+  const __half2 h = __floats2half2_rn(x, y);
+  const float2 f = __half22float2(h);
+  hi = *reinterpret_cast<const uint32_t*>(&h);
+  lo = pack_half2(x - f.x, y - f.y);
+}
+
+// Byte offset of byte d of cell c's row in a stage: 32-byte pairs swizzled by the cell.
+__device__ __forceinline__ int pd_koff(int c, int d) { return c * kD + (d ^ ((c & 7) << 5)); }
+__device__ __forceinline__ int pd_voff(int c, int d) { return c * kD + (d ^ (((c >> 1) & 7) << 5)); }
+
+// One row of 8 output values: o * inv, gated, in T.
+template <typename T>
+__device__ __forceinline__ void pd_write8(const PdArgs& a, int row, int head, int d, float (&x)[8], float inv) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) x[e] *= inv;
+  if (a.gate) {
+    Row8<T> graw;
+    graw.load(static_cast<const T*>(a.gate) + row * a.ldg + head * kD + d);
+    float g[8];
+    graw.get(g);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] *= gate_factor(g[e]);
+  }
+  Row8<T>::store(static_cast<T*>(a.out) + row * a.ldo + head * kD + d, x);
+}
+
+template <int MT, int C, int STAGES, bool kSplit>
+struct PdSmem {
+  static constexpr int kStageBytes = C * STAGES * static_cast<int>(sizeof(PdStage));
+  static constexpr int kJoinBytes = C * MT * 16 * (kD + 4) * 4;  // rows padded to 260 floats
+  static constexpr int kQBytes = MT * 16 * kD * 2 * (kSplit ? 2 : 1);
+  static constexpr int kStatBytes = C * MT * 16 * 8;
+  static constexpr int kBytes = kQBytes + kStatBytes + (kStageBytes > kJoinBytes ? kStageBytes : kJoinBytes);
+};
+
+// grid: CTAs that share the flat block list; block: 32 * MT * C.
+template <typename T, int MT, int C, int STAGES, int MINB>
+__global__ void __launch_bounds__(32 * MT * C, MINB) paged_decode_kernel(PdArgs a) {
+  constexpr bool kSplit = sizeof(T) == 4;
+  constexpr int NT = 32 * MT * C, GT = 32 * MT;  // threads of the CTA, of a group
+  constexpr int CB = 16 * C;                     // cells of a block of the flat list
+  using Smem = PdSmem<MT, C, STAGES, kSplit>;
+  extern __shared__ __align__(16) unsigned char smem_raw[];
+  uint4* sq = reinterpret_cast<uint4*>(smem_raw);  // [MT][hi, lo][16 k-steps][32 lanes]
+  float2* sstat = reinterpret_cast<float2*>(smem_raw + Smem::kQBytes);
+  PdStage* stages = reinterpret_cast<PdStage*>(smem_raw + Smem::kQBytes + Smem::kStatBytes);
+  float* sjoin = reinterpret_cast<float*>(stages);
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int mt = warp % MT, cg = warp / MT;
+  const int gtid = tid - cg * GT;
+  const int g = lane >> 2, t = lane & 3;
+  const int hkv = a.c.hkv;
+  PdStage* ring = stages + cg * STAGES;
+
+  griddep_wait();
+
+  // ---- this CTA's range of the flat list, and the unit it starts in (every warp the same)
+  int total = 0;
+  for (int s0 = 0; s0 < a.b.nseq; s0 += 32) {
+    const int s = s0 + lane;
+    total += s < a.b.nseq ? (pd_seq(a, s).cells + CB - 1) / CB : 0;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  total *= hkv;
+  const int per = max(1, (total + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x));
+  const int from = min(total, static_cast<int>(blockIdx.x) * per), to = min(total, from + per);
+  griddep_launch();  // the join waits for this grid before it reads anything
+  if (from >= to) return;
+  int seq = 0, before = 0;  // before: blocks of the sequences in front of `seq`
+  for (int s0 = 0, base = 0; s0 < a.b.nseq; s0 += 32) {
+    const int s = s0 + lane;
+    const int nb = s < a.b.nseq ? (pd_seq(a, s).cells + CB - 1) / CB * hkv : 0;
+    int inc = nb;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += y;
+    }
+    const uint32_t past = __ballot_sync(0xffffffffu, base + inc > from);
+    if (past) {
+      const int l = __ffs(past) - 1;
+      seq = s0 + l;
+      before = base + __shfl_sync(0xffffffffu, inc - nb, l);
+      break;
+    }
+    base += __shfl_sync(0xffffffffu, inc, 31);
+  }
+
+  // ---- one (sequence, KV head) after the other
+  int at = from;
+  PdSeq q = pd_seq(a, seq);
+  int nb = (q.cells + CB - 1) / CB;
+  while (at < to) {
+    while (at >= before + nb * hkv) {  // sequences without cells have no blocks
+      before += nb * hkv;
+      q = pd_seq(a, ++seq);
+      nb = (q.cells + CB - 1) / CB;
+    }
+    const int kvh = (at - before) / nb;
+    const int u0 = before + kvh * nb;          // the unit's blocks in the flat list
+    const int blk0 = at - u0, blk1 = min(nb, to - u0);
+    at = u0 + blk1;
+    const int unit = seq * hkv + kvh;
+    const int first_cta = u0 / per, pieces = (u0 + nb - 1) / per - first_cta + 1;
+    if (blk0 == 0 && tid == 0) a.unit[unit] = make_int2(first_cta, pieces);
+    const int nrow = min(q.n, a.max_q) * a.group;
+
+    // ---- the first stages' cells, then Q as MMA fragments
+    // A block's 16 cells: lane l < 16 looks up cell l; the lookups run a block ahead.
+    auto lookup = [&](int blk) {
+      const int p = (blk * C + cg) * 16 + (lane & 15);
+      return blk < blk1 && p < q.cells ? batch_cell(a.b, seq, p) : -1;
+    };
+    auto fetch = [&](PdStage& st, int cell) {  // cell: this lane's lookup
+#pragma unroll
+      for (int u = 0; u < (256 + GT - 1) / GT; ++u) {
+        const int chunk = gtid + GT * u;
+        const int i = (chunk >> 4) & 15, part = (chunk & 15) * 16;
+        const int ci = __shfl_sync(0xffffffffu, cell, i);
+        if (256 % GT == 0 || chunk < 256) {
+          const size_t row = (static_cast<size_t>(max(ci, 0)) * hkv + kvh) * kD + part;
+          cp_async16(st.k + pd_koff(i, part), a.c.k + row, ci >= 0);
+          cp_async16(st.v + pd_voff(i, part), a.c.v + row, ci >= 0);
+        }
+      }
+      const int ci = __shfl_sync(0xffffffffu, cell, gtid & 15);
+      if (gtid < 32) {
+        const size_t row = (static_cast<size_t>(max(ci, 0)) * hkv + kvh) * kNG;
+        if (gtid < 16) cp_async16(st.ks + gtid * kNG, a.c.ks + row, ci >= 0);
+        else cp_async16(st.vs + (gtid - 16) * kNG, a.c.vs + row, ci >= 0);
+      }
+    };
+    int look[STAGES];  // look[i]: cells of the block i ahead of the one being computed
+#pragma unroll
+    for (int i = 0; i < STAGES; ++i) look[i] = lookup(blk0 + i);
+#pragma unroll
+    for (int i = 0; i < STAGES - 1; ++i) {
+      if (blk0 + i < blk1) fetch(ring[i], look[i]);
+      cp_async_commit();
+    }
+    for (int e = tid; e < MT * 16 * 32; e += NT) {
+      const int l = e & 31, ks = (e >> 5) & 15, m = e >> 9;
+      const int d0 = 32 * (ks >> 1) + 8 * (l & 3) + 4 * (ks & 1);
+      uint32_t hi[4], lo[4];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {  // rows g and g + 8 of the tile
+        const int r = m * 16 + (l >> 2) + 8 * h;
+        float x[4] = {0.f, 0.f, 0.f, 0.f};
+        if (r < nrow) {
+          const int tok = r / a.group, head = kvh * a.group + r - tok * a.group;
+          const T* src = static_cast<const T*>(a.q) + (q.row0 + tok) * a.ldq + head * kD + d0;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x[i] = pd_to_float(src[i]);
+        }
+        if constexpr (kSplit) {
+          pd_split2(x[0], x[1], hi[h], lo[h]);
+          pd_split2(x[2], x[3], hi[h + 2], lo[h + 2]);
+        } else {
+          hi[h] = pack_half2(x[0], x[1]);
+          hi[h + 2] = pack_half2(x[2], x[3]);
+        }
+      }
+      uint4* dst = sq + (m * (kSplit ? 2 : 1) * 16 + ks) * 32 + l;
+      dst[0] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+      if constexpr (kSplit) dst[16 * 32] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    }
+    // cells that the thread's two rows see, and that every row of the tile sees
+    int vis[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) vis[r] = pd_visible(q, min((mt * 16 + g + 8 * r) / a.group, q.n - 1));
+    const int vis_all = pd_visible(q, min(mt * 16 / a.group, q.n - 1));
+    __syncthreads();
+
+    float m_run[2] = {kAttnNoMax, kAttnNoMax}, l_run[2] = {0.f, 0.f};
+    float o[kNG][4][4];
+#pragma unroll
+    for (int gi = 0; gi < kNG; ++gi)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) o[gi][i][c] = 0.f;
+    const uint4* mq = sq + mt * (kSplit ? 2 : 1) * 16 * 32 + lane;
+
+    int slot = 0;
+    for (int blk = blk0; blk < blk1; ++blk) {
+      // block blk has landed for this thread; after the barrier for the group, and every
+      // warp of it has left block blk - 1, whose stage the fetch below refills
+      cp_async_wait<STAGES - 2>();
+      if constexpr (MT == 1) __syncwarp();
+      else asm volatile("bar.sync %0, %1;\n" ::"r"(1 + cg), "n"(GT) : "memory");
+      const int next = lookup(blk + STAGES);
+      if (blk + STAGES - 1 < blk1) fetch(ring[slot == 0 ? STAGES - 1 : slot - 1], look[STAGES - 1]);
+      cp_async_commit();
+      const PdStage& st = ring[slot];
+      slot = slot + 1 == STAGES ? 0 : slot + 1;
+      const uint32_t valid = __ballot_sync(0xffffffffu, look[0] >= 0) & 0xffffu;
+#pragma unroll
+      for (int i = 0; i + 1 < STAGES; ++i) look[i] = look[i + 1];
+      look[STAGES - 1] = next;
+      const int p0 = (blk * C + cg) * 16;
+      if (valid == 0u) continue;
+
+      // ---- scores of 16 cells: two n-tiles of 8
+      float s[2][4];
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) s[nt][c] = 0.f;
+      uint4 ksw[2][2];  // the 8 scales of cells 8 nt + 2t and 8 nt + 2t + 1
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) ksw[nt][c] = *reinterpret_cast<const uint4*>(st.ks + (8 * nt + 2 * t + c) * kNG);
+#pragma unroll
+      for (int qg = 0; qg < kNG; ++qg) {
+        const uint4 qa = mq[(2 * qg) * 32], qb = mq[(2 * qg + 1) * 32];
+        const uint32_t a0[4] = {qa.x, qa.y, qa.z, qa.w}, a1[4] = {qb.x, qb.y, qb.z, qb.w};
+        uint32_t c0[4], c1[4];
+        if constexpr (kSplit) {
+          const uint4 la = mq[(16 + 2 * qg) * 32], lb = mq[(16 + 2 * qg + 1) * 32];
+          c0[0] = la.x, c0[1] = la.y, c0[2] = la.z, c0[3] = la.w;
+          c1[0] = lb.x, c1[1] = lb.y, c1[2] = lb.z, c1[3] = lb.w;
+        }
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt) {
+          const uint2 kw = *reinterpret_cast<const uint2*>(st.k + pd_koff(8 * nt + g, 32 * qg + 8 * t));
+          const uint32_t x0 = kw.x ^ 0x80808080u, x1 = kw.y ^ 0x80808080u;
+          const uint32_t b00 = i8x2_to_h2(x0, 0x4140u), b01 = i8x2_to_h2(x0, 0x4342u);
+          const uint32_t b10 = i8x2_to_h2(x1, 0x4140u), b11 = i8x2_to_h2(x1, 0x4342u);
+          float acc[4] = {0.f, 0.f, 0.f, 0.f};
+          if constexpr (kSplit) {
+            mma_f16_16816(acc, c0, b00, b01);
+            mma_f16_16816(acc, c1, b10, b11);
+          }
+          mma_f16_16816(acc, a0, b00, b01);
+          mma_f16_16816(acc, a1, b10, b11);
+          const uint32_t wa = (&ksw[nt][0].x)[qg >> 1], wb = (&ksw[nt][1].x)[qg >> 1];
+          const __half2 ha = *reinterpret_cast<const __half2*>(&wa), hb = *reinterpret_cast<const __half2*>(&wb);
+          const float sa = (qg & 1) ? __high2float(ha) : __low2float(ha);
+          const float sb = (qg & 1) ? __high2float(hb) : __low2float(hb);
+          s[nt][0] = fmaf(sa, acc[0], s[nt][0]);
+          s[nt][1] = fmaf(sb, acc[1], s[nt][1]);
+          s[nt][2] = fmaf(sa, acc[2], s[nt][2]);
+          s[nt][3] = fmaf(sb, acc[3], s[nt][3]);
+        }
+      }
+      // ---- masks, running maximum, weights
+      float mx[2] = {-INFINITY, -INFINITY};
+      const bool masked = valid != 0xffffu || p0 + 16 > vis_all;
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          float x = s[nt][c] * a.scale_log2;
+          if (masked) {
+            const int i = 8 * nt + 2 * t + (c & 1);
+            if (!((valid >> i) & 1u) || p0 + i >= vis[c >> 1]) x = -INFINITY;
+          }
+          s[nt][c] = x;
+          mx[c >> 1] = fmaxf(mx[c >> 1], x);
+        }
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
+        mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
+      }
+      // The reference maximum moves only by more than 2^8, so P stays within fp16 and most
+      // blocks skip the rescale.
+      if (__any_sync(0xffffffffu, mx[0] > m_run[0] + kAttnShift || mx[1] > m_run[1] + kAttnShift)) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const float mnew = fmaxf(m_run[r], mx[r]);
+          const float alpha = attn_exp2(m_run[r] - mnew);
+          l_run[r] *= alpha;
+          m_run[r] = mnew;
+#pragma unroll
+          for (int gi = 0; gi < kNG; ++gi)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              o[gi][i][2 * r] *= alpha;
+              o[gi][i][2 * r + 1] *= alpha;
+            }
+        }
+      }
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          s[nt][c] = attn_exp2(s[nt][c] - m_run[c >> 1]);
+          l_run[c >> 1] += s[nt][c];  // this thread's columns; summed over the quad at the end
+        }
+
+      // ---- P V: k-index j of P is cell j
+      uint32_t ph[4], pl[4];
+      if constexpr (kSplit) {
+        pd_split2(s[0][0], s[0][1], ph[0], pl[0]);
+        pd_split2(s[0][2], s[0][3], ph[1], pl[1]);
+        pd_split2(s[1][0], s[1][1], ph[2], pl[2]);
+        pd_split2(s[1][2], s[1][3], ph[3], pl[3]);
+      } else {
+        ph[0] = pack_half2(s[0][0], s[0][1]);
+        ph[1] = pack_half2(s[0][2], s[0][3]);
+        ph[2] = pack_half2(s[1][0], s[1][1]);
+        ph[3] = pack_half2(s[1][2], s[1][3]);
+      }
+      uint4 vsw[4];  // the scales of cells 2t, 2t+1, 2t+8, 2t+9
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        vsw[j] = *reinterpret_cast<const uint4*>(st.vs + (2 * t + (j & 1) + 8 * (j >> 1)) * kNG);
+#pragma unroll
+      for (int gi = 0; gi < kNG; ++gi) {
+        const int d = 32 * gi + 4 * g;  // column g of n-tile i is dim 32 gi + 4 g + i
+        const uint32_t wA = *reinterpret_cast<const uint32_t*>(st.v + pd_voff(2 * t, d)) ^ 0x80808080u;
+        const uint32_t wB = *reinterpret_cast<const uint32_t*>(st.v + pd_voff(2 * t + 1, d)) ^ 0x80808080u;
+        const uint32_t wC = *reinterpret_cast<const uint32_t*>(st.v + pd_voff(2 * t + 8, d)) ^ 0x80808080u;
+        const uint32_t wD = *reinterpret_cast<const uint32_t*>(st.v + pd_voff(2 * t + 9, d)) ^ 0x80808080u;
+        const uint32_t hsel = (gi & 1) ? 0x7632u : 0x5410u;
+        const uint32_t uAB = __byte_perm((&vsw[0].x)[gi >> 1], (&vsw[1].x)[gi >> 1], hsel);
+        const uint32_t uCD = __byte_perm((&vsw[2].x)[gi >> 1], (&vsw[3].x)[gi >> 1], hsel);
+        const __half2 sAB = *reinterpret_cast<const __half2*>(&uAB);
+        const __half2 sCD = *reinterpret_cast<const __half2*>(&uCD);
+        const uint32_t ab[2] = {__byte_perm(wA, wB, 0x5140u), __byte_perm(wA, wB, 0x7362u)};
+        const uint32_t cd[2] = {__byte_perm(wC, wD, 0x5140u), __byte_perm(wC, wD, 0x7362u)};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t sel = (i & 1) ? 0x4342u : 0x4140u;
+          const uint32_t b0 = i8x2_to_h2(ab[i >> 1], sel), b1 = i8x2_to_h2(cd[i >> 1], sel);
+          const __half2 f0 = *reinterpret_cast<const __half2*>(&b0), f1 = *reinterpret_cast<const __half2*>(&b1);
+          const __half2 h0 = __hmul2(f0, sAB), h1 = __hmul2(f1, sCD);
+          const uint32_t v0 = *reinterpret_cast<const uint32_t*>(&h0), v1 = *reinterpret_cast<const uint32_t*>(&h1);
+          if constexpr (kSplit) {
+            // code * vs - fp16(code * vs), exact by the fused multiply-add
+            const __half2 r0 = __hfma2(f0, sAB, __hneg2(h0)), r1 = __hfma2(f1, sCD, __hneg2(h1));
+            mma_f16_16816(o[gi][i], ph, *reinterpret_cast<const uint32_t*>(&r0),
+                          *reinterpret_cast<const uint32_t*>(&r1));
+            mma_f16_16816(o[gi][i], pl, v0, v1);
+          }
+          mma_f16_16816(o[gi][i], ph, v0, v1);
+        }
+      }
+    }
+    cp_async_wait<0>();
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      l_run[r] += __shfl_xor_sync(0xffffffffu, l_run[r], 1);
+      l_run[r] += __shfl_xor_sync(0xffffffffu, l_run[r], 2);
+    }
+
+    // ---- the C groups join in shared memory (the stages are free: every copy has landed)
+    __syncthreads();
+    constexpr int kRow = kD + 4;  // floats of a joined row
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int row = (cg * MT + mt) * 16 + g + 8 * r;
+      if (t == 0) sstat[row] = make_float2(l_run[r] > 0.f ? m_run[r] : -INFINITY, l_run[r]);
+#pragma unroll
+      for (int gi = 0; gi < kNG; ++gi) {
+        // C element (row, col 2t) of n-tile i, group gi is dim 32 gi + 8 t + i; col 2t+1 is +4
+        float* dst = sjoin + row * kRow + 32 * gi + 8 * t;
+        *reinterpret_cast<float4*>(dst) =
+            make_float4(o[gi][0][2 * r], o[gi][1][2 * r], o[gi][2][2 * r], o[gi][3][2 * r]);
+        *reinterpret_cast<float4*>(dst + 4) =
+            make_float4(o[gi][0][2 * r + 1], o[gi][1][2 * r + 1], o[gi][2][2 * r + 1], o[gi][3][2 * r + 1]);
+      }
+    }
+    __syncthreads();
+    const size_t slot_row = (2 * static_cast<size_t>(blockIdx.x) + (blk0 == 0 ? 1 : 0)) * a.prows;
+    for (int row = warp; row < nrow; row += MT * C) {
+      float2 st[C];
+      float top = -INFINITY, l = 0.f, x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        st[c] = sstat[c * MT * 16 + row];
+        top = fmaxf(top, st[c].x);
+      }
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        const float w = st[c].y > 0.f ? attn_exp2(st[c].x - top) : 0.f;
+        l = fmaf(w, st[c].y, l);
+        const float4* src = reinterpret_cast<const float4*>(sjoin + (c * MT * 16 + row) * kRow + 8 * lane);
+        const float4 lo = src[0], hi = src[1];
+        x[0] = fmaf(w, lo.x, x[0]), x[1] = fmaf(w, lo.y, x[1]), x[2] = fmaf(w, lo.z, x[2]), x[3] = fmaf(w, lo.w, x[3]);
+        x[4] = fmaf(w, hi.x, x[4]), x[5] = fmaf(w, hi.y, x[5]), x[6] = fmaf(w, hi.z, x[6]), x[7] = fmaf(w, hi.w, x[7]);
+      }
+      if (pieces == 1) {
+        const int tok = row / a.group;
+        pd_write8<T>(a, q.row0 + tok, kvh * a.group + row - tok * a.group, 8 * lane, x, l > 0.f ? 1.f / l : 0.f);
+      } else {
+        Row8<float>::store(a.part_o + (slot_row + row) * kD + 8 * lane, x);
+        if (lane == 0) a.part_ml[slot_row + row] = make_float2(top, l);
+      }
+    }
+    __syncthreads();  // the next unit's cells and Q reuse this memory
+  }
+}
+
+constexpr int kPjWarps = 8;
+
+// Joins the pieces of one packed row and head (and writes the zeros of rows whose sequence has
+// no cells).  grid: (rows, hq); block: 256.  Pieces spread over 8 warps; each lane 8 dims.
+template <typename T>
+__global__ void __launch_bounds__(32 * kPjWarps) paged_join_kernel(PdArgs a) {
+  __shared__ float so[kPjWarps][kD + 4];
+  __shared__ float sm[kPjWarps], sl[kPjWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int row = blockIdx.x, head = blockIdx.y;
+  griddep_wait();
+  const int s = batch_find(a.b, row, lane);
+  if (s < 0) return;
+  const PdSeq q = pd_seq(a, s);
+  const int tok = row - q.row0;
+  if (tok >= a.max_q) return;
+  float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  if (q.cells == 0) {
+    if (warp == 0) pd_write8<T>(a, row, head, 8 * lane, x, 0.f);
+    return;
+  }
+  const int kvh = head / a.group, unit = s * a.c.hkv + kvh;
+  const int2 info = __ldcg(a.unit + unit);
+  if (info.y == 1) return;  // written by its CTA
+  const size_t in_slot = static_cast<size_t>(tok) * a.group + head - kvh * a.group;
+  // each warp its pieces, online
+  float top = -INFINITY, l = 0.f;
+  for (int j0 = warp; j0 < info.y; j0 += 4 * kPjWarps) {
+    float2 ml[4];
+    float4 lo[4], hi[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int j = j0 + u * kPjWarps;
+      ml[u] = make_float2(-INFINITY, 0.f);
+      lo[u] = hi[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (j < info.y) {
+        const size_t r = (2 * static_cast<size_t>(info.x + j) + (j == 0 ? 1 : 0)) * a.prows + in_slot;
+        ml[u] = __ldcg(a.part_ml + r);
+        const float4* src = reinterpret_cast<const float4*>(a.part_o + r * kD + 8 * lane);
+        lo[u] = __ldcg(src);
+        hi[u] = __ldcg(src + 1);
+      }
+    }
+    float mnew = top;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) mnew = fmaxf(mnew, ml[u].x);
+    if (mnew == -INFINITY) continue;
+    const float alpha = attn_exp2(top - mnew);
+    top = mnew;
+    l *= alpha;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] *= alpha;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const float w = ml[u].y > 0.f ? attn_exp2(ml[u].x - mnew) : 0.f;
+      l = fmaf(w, ml[u].y, l);
+      x[0] = fmaf(w, lo[u].x, x[0]), x[1] = fmaf(w, lo[u].y, x[1]);
+      x[2] = fmaf(w, lo[u].z, x[2]), x[3] = fmaf(w, lo[u].w, x[3]);
+      x[4] = fmaf(w, hi[u].x, x[4]), x[5] = fmaf(w, hi[u].y, x[5]);
+      x[6] = fmaf(w, hi[u].z, x[6]), x[7] = fmaf(w, hi[u].w, x[7]);
+    }
+  }
+  Row8<float>::store(&so[warp][8 * lane], x);
+  if (lane == 0) sm[warp] = top, sl[warp] = l;
+  __syncthreads();
+  if (warp != 0) return;
+  float all = -INFINITY, total = 0.f;
+#pragma unroll
+  for (int w = 0; w < kPjWarps; ++w) all = fmaxf(all, sm[w]);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) x[e] = 0.f;
+#pragma unroll
+  for (int w = 0; w < kPjWarps; ++w) {
+    const float e = sl[w] > 0.f ? attn_exp2(sm[w] - all) : 0.f;
+    total = fmaf(e, sl[w], total);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = fmaf(e, so[w][8 * lane + i], x[i]);
+  }
+  pd_write8<T>(a, row, head, 8 * lane, x, total > 0.f ? 1.f / total : 0.f);
+}
+
+}  // namespace qsa

@@ -40,6 +40,10 @@ SIGNATURES = {
     "qsa_attn": (_I, [_P, _I, _P, _P, _I, _I, _F, _P, _P, _P, _P]),
     "qsa_merge": (_I, [_P, _I, _I, _P, _P, _P]),
     "qsa_topk_static": (_I, [_P, _I64, _I, _I, _I, _P, _P]),
+    "qsa_paged_write": (_I, [_P, _P, _I, _I, _P, _I64, _P, _I64, _P]),
+    "qsa_paged_read": (_I, [_P, _P, _I, _I, _P, _I64, _P, _I64, _P]),
+    "qsa_paged_decode_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I]),
+    "qsa_paged_decode": (_I, [_P, _P, _I, _I, _I, _I, _I, _P, _I64, _P, _I64, _F, _P, _SZ, _P, _I64, _P]),
     "qsa_device_status": (_I, [_P, _P]),
     "qsa_selftest_wait_timeout": (_I, [_P]),
     "qsa_trace_begin": (_I, [_I, _P]),
@@ -281,6 +285,191 @@ def merge(part, out=None, stream=None, gate=None):
     _check(load().qsa_merge(_ptr(_dev(part, torch.float32, "part")), rows, nsplit,
                             _opt(gate, torch.float32, "gate"), _ptr(_dev(out, torch.float32, "out")),
                             _stream(stream)))
+    return out
+
+
+# ---- batches of sequences: paged cache, its decode attention, packed prompts
+
+_DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+
+
+class PagedCacheStruct(ctypes.Structure):
+    _fields_ = [("k", _P), ("v", _P), ("ks", _P), ("vs", _P), ("pages", ctypes.c_int32),
+                ("page_cells", ctypes.c_int32), ("hkv", ctypes.c_int32)]
+
+
+class BatchStruct(ctypes.Structure):
+    _fields_ = [("table", _P), ("kv_len", _P), ("cu_q", _P), ("nseq", ctypes.c_int32), ("table_ld", ctypes.c_int32)]
+
+
+class PagedCache:
+    """A pool of cache pages (layout of ``qsa_paged_cache``): k, v int8
+    [pages][page_cells][hkv][256]; ks, vs float16 [pages][page_cells][hkv][8]."""
+
+    def __init__(self, k, v, ks, vs):
+        for t, dtype, name, last in ((k, torch.int8, "k", D), (v, torch.int8, "v", D),
+                                     (ks, torch.float16, "ks", NG), (vs, torch.float16, "vs", NG)):
+            _dev(t, dtype, name)
+            if t.dim() != 4 or t.shape[:3] != k.shape[:3] or t.shape[3] != last:
+                raise ValueError(f"{name} must be [pages][page_cells][hkv][{last}], got {tuple(t.shape)}")
+            if t.device != k.device:
+                raise ValueError(f"{name} is on {t.device}, k on {k.device}")
+        self.k, self.v, self.ks, self.vs = k, v, ks, vs
+        self.pages, self.page_cells, self.hkv = k.shape[:3]
+        self.device = k.device
+        self._struct = PagedCacheStruct(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), self.pages,
+                                        self.page_cells, self.hkv)
+        self._ref = ctypes.addressof(self._struct)
+
+    @staticmethod
+    def empty(pages: int, page_cells: int, hkv: int = HKV, device="cuda") -> "PagedCache":
+        def z(last, dtype):
+            return torch.zeros(pages, page_cells, hkv, last, dtype=dtype, device=device)
+        return PagedCache(z(D, torch.int8), z(D, torch.int8), z(NG, torch.float16), z(NG, torch.float16))
+
+
+class Batch:
+    """The sequences of a batched call (``qsa_batch``), int32 CUDA tensors: table
+    [nseq][width] pages, kv_len [nseq], cu_q [nseq + 1] or None (one row per sequence).
+    The tensors are read when the kernels run: update them in place between calls."""
+
+    def __init__(self, table, kv_len, cu_q=None):
+        _dev(table, torch.int32, "table")
+        _dev(kv_len, torch.int32, "kv_len")
+        if table.dim() != 2 or kv_len.dim() != 1 or table.shape[0] != kv_len.shape[0]:
+            raise ValueError(f"table must be [nseq][width] and kv_len [nseq], got {tuple(table.shape)}, "
+                             f"{tuple(kv_len.shape)}")
+        if cu_q is not None:
+            _dev(cu_q, torch.int32, "cu_q")
+            if cu_q.dim() != 1 or cu_q.shape[0] != kv_len.shape[0] + 1:
+                raise ValueError(f"cu_q must be [nseq + 1], got {tuple(cu_q.shape)}")
+        for t, name in ((kv_len, "kv_len"), (cu_q, "cu_q")):
+            if t is not None and t.device != table.device:
+                raise ValueError(f"{name} is on {t.device}, table on {table.device}")
+        self.table, self.kv_len, self.cu_q = table, kv_len, cu_q
+        self.nseq, self.width = table.shape
+        self.device = table.device
+        self._struct = BatchStruct(table.data_ptr(), kv_len.data_ptr(), _ptr(cu_q), self.nseq, self.width)
+        self._ref = ctypes.addressof(self._struct)
+
+
+def _packed(t, heads, dtype, device, name):
+    """(pointer, row stride) of packed rows [rows][heads][256] whose heads are contiguous."""
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the call on {device}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    n, h, d = t.shape
+    ld, sh, sd = t.stride()
+    if h != heads or d != D:
+        raise ValueError(f"{name} must be [rows][{heads}][{D}], got {tuple(t.shape)}")
+    if sd != 1 or (h > 1 and sh != D):
+        raise ValueError(f"{name}: a row's {heads} x {D} values must be contiguous, strides {t.stride()}")
+    return t.data_ptr(), ld if n > 1 else heads * D
+
+
+def _same_rows(t, rows, name):
+    if t.shape[0] != rows:
+        raise ValueError(f"{name} has {t.shape[0]} rows, the call has {rows}")
+
+
+class _On:
+    """The device of a call's tensors as the current one, and `stream` as torch's current
+    stream there (for what the call allocates); a no-op where both are already so."""
+    __slots__ = ("dev", "stream", "held")
+
+    def __init__(self, device, stream):
+        self.dev, self.stream, self.held = device, stream, ()
+
+    def __enter__(self):
+        if self.dev.index != torch.cuda.current_device():
+            self.held = (torch.cuda.device(self.dev),)
+        if self.stream is not None:
+            self.held += (torch.cuda.stream(self.stream),)
+        for c in self.held:
+            c.__enter__()
+
+    def __exit__(self, *exc):
+        for c in reversed(self.held):
+            c.__exit__(*exc)
+        return False
+
+
+def _dtype_code(dtype):
+    code = _DTYPES.get(dtype)
+    if code is None:
+        raise ValueError(f"rows must be float32, float16 or bfloat16, got {dtype}")
+    return code
+
+
+def _batch_on(cache, batch):
+    if batch.device != cache.device:
+        raise ValueError(f"the batch is on {batch.device}, the cache on {cache.device}")
+
+
+def paged_write(cache: PagedCache, batch: Batch, k, v, stream=None) -> None:
+    """Quantise packed rows k, v [rows][hkv][256] (float32, float16 or bfloat16; row strides
+    free) into the cells of the batch's positions."""
+    _batch_on(cache, batch)
+    code = _dtype_code(k.dtype)
+    rows = k.shape[0]
+    kp, ldk = _packed(k, cache.hkv, k.dtype, cache.device, "k")
+    vp, ldv = _packed(v, cache.hkv, k.dtype, cache.device, "v")
+    _same_rows(v, rows, "v")
+    with _On(cache.device, None):
+        _check(load().qsa_paged_write(cache._ref, batch._ref, rows, code, kp, ldk, vp, ldv, _stream(stream)))
+
+
+def paged_read(cache: PagedCache, batch: Batch, rows: int, dtype=torch.float16, k=None, v=None, stream=None):
+    """(k, v) [rows][hkv][256]: the batch's cells as values, rounded once to dtype.  Rows of
+    no sequence are left as they were (undefined in arrays that this call allocates)."""
+    _batch_on(cache, batch)
+    code = _dtype_code(dtype)
+    with _On(cache.device, stream):
+        if k is None:
+            k = torch.empty(rows, cache.hkv, D, dtype=dtype, device=cache.device)
+        if v is None:
+            v = torch.empty(rows, cache.hkv, D, dtype=dtype, device=cache.device)
+        kp, ldk = _packed(k, cache.hkv, dtype, cache.device, "k")
+        vp, ldv = _packed(v, cache.hkv, dtype, cache.device, "v")
+        _same_rows(k, rows, "k")
+        _same_rows(v, rows, "v")
+        _check(load().qsa_paged_read(cache._ref, batch._ref, rows, code, kp, ldk, vp, ldv, _stream(stream)))
+    return k, v
+
+
+def paged_decode_workspace_bytes(nseq: int, hq: int, hkv: int, max_q: int, max_len: int) -> int:
+    return int(load().qsa_paged_decode_workspace_bytes(nseq, hq, hkv, max_q, max_len))
+
+
+def paged_decode(cache: PagedCache, batch: Batch, q, scale: float = 1 / 16, max_q: int = 1, max_len=None, gate=None,
+                 out=None, ws=None, stream=None):
+    """Attention of each sequence's newest rows (at most max_q) over all its cells, at most
+    max_len (default: what the table can hold).  q, gate, out: [rows][hq][256] of one type.
+    Rows of no sequence are left as they were (undefined in an output allocated here)."""
+    _batch_on(cache, batch)
+    code = _dtype_code(q.dtype)
+    rows, hq = q.shape[0], q.shape[1]
+    dev, dtype = cache.device, q.dtype
+    if max_len is None:
+        max_len = min(batch.width * cache.page_cells, (1 << 31) - 1)
+    qp, ldq = _packed(q, hq, dtype, dev, "q")
+    gp, ldg = (None, 0) if gate is None else _packed(gate, hq, dtype, dev, "gate")
+    if gate is not None:
+        _same_rows(gate, rows, "gate")
+    lib = load()
+    with _On(dev, stream):
+        if out is None:
+            out = torch.empty(rows, hq, D, dtype=dtype, device=dev)
+        op, ldo = _packed(out, hq, dtype, dev, "out")
+        _same_rows(out, rows, "out")
+        if ws is None:
+            need = lib.qsa_paged_decode_workspace_bytes(batch.nseq, hq, cache.hkv, max_q, max_len)
+            ws = torch.empty(need or 16, dtype=torch.uint8, device=dev)
+        elif ws.device != dev or not ws.is_contiguous():
+            raise ValueError(f"ws must be contiguous on {dev}")
+        _check(lib.qsa_paged_decode(cache._ref, batch._ref, rows, max_q, max_len, code, hq, qp, ldq, gp, ldg, scale,
+                                    ws.data_ptr(), ws.numel() * ws.element_size(), op, ldo, _stream(stream)))
     return out
 
 
