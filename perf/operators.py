@@ -211,8 +211,7 @@ def prepare(case, seed):
 def _own(st):
     from top_sparse_attention_score_b200 import qsa
     if st["op"] == "prompt":
-        return qsa.prompt_attn(st["q"], st["k"], st["v"], st["cu_q"], st["cu_k"], st["max_q"], scale=SCALE,
-                               gate=st["gate"])
+        return qsa.prompt_attn(st["q"], st["k"], st["v"], st["cu_q"], st["cu_k"], scale=SCALE, gate=st["gate"])
     if "cache" not in st:  # a server keeps its cache and its batch
         st["cache"] = qsa.PagedCache(st["ck"], st["cv"], st["ks"], st["vs"])
         st["batch"] = qsa.Batch(st["table"], st["kv_len"], st["cu"])
