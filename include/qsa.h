@@ -363,6 +363,23 @@ int qsa_paged_decode(const qsa_paged_cache* cache, const qsa_batch* batch, int r
                      void* stream);
 
 /*
+ * Causal attention over whole prompts, packed one after the other: sequence s has the query
+ * rows cu_q[s] .. cu_q[s+1] - 1 and the key rows cu_k[s] .. cu_k[s+1] - 1 ([nseq + 1] each,
+ * ascending from 0, device memory; the same array for prompts without a cached prefix).  The
+ * queries are the last positions: row i of n against m keys sees keys j <= i + m - n,
+ *   out[r][h] = softmax_j(scale * q[r][h] . k[j][h / (hq / hkv)]) . v[j]   (* sigmoid(gate[r][h]))
+ * and is 0 when it sees none.  q, gate (or NULL), out [rows_q][hq][256] and k, v
+ * [rows_k][hkv][256] of QSA_F16 or QSA_BF16 (the tensor cores' types: fp32 rows are refused,
+ * fp32 callers cast or use the paged cache).  Rows at or past cu_q[nseq] are left as they were;
+ * what lies behind a sequence's keys is not used, whatever it holds.  Waits are bounded and
+ * report through qsa_device_status.
+ */
+int qsa_prompt_attn(int nseq, const int32_t* cu_q, const int32_t* cu_k, int rows_q, int rows_k,
+                    int dtype, int hq, int hkv, const void* q, int64_t ldq, const void* k,
+                    int64_t ldk, const void* v, int64_t ldv, const void* gate, int64_t ldg,
+                    float scale, void* out, int64_t ldo, void* stream);
+
+/*
  * Device-side failure report.  Kernels that wait on an mbarrier (the prefill
  * score GEMM) bound every wait to four seconds; on expiry they stop, drain their
  * copies, free their tensor memory and record QSA_ERR_TIMEOUT in a status word

@@ -3,10 +3,12 @@
 // launches; the computation is in the kernels of the qsa_paged_*.cuh and qsa_prompt_attn.cuh files.
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "qsa_host.h"
 #include "qsa_paged_cache.cuh"
 #include "qsa_paged_decode.cuh"
+#include "qsa_prompt_attn.cuh"
 
 using namespace qsa::host;
 
@@ -162,6 +164,40 @@ int launch_decode(const qsa::PdArgs& a, const DecodePlan& p, int hq, cudaStream_
   return launched("paged_join_kernel", launch_pdl(qsa::paged_join_kernel<T>, dim3(a.rows, hq), dim3(32 * qsa::kPjWarps), 0, s, a));
 }
 
+// Tensor map of packed rows [rows][heads][256] of a 16-bit type: boxes of 64 dims of one head
+// of `box_rows` rows, 128-byte swizzle.  Rows past the end read as 0.
+int encode_rows(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap* map, const char* name, const void* p, int dtype,
+                int rows, int heads, int64_t ld, int box_rows) {
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(QSA_D), static_cast<cuuint64_t>(heads),
+                              static_cast<cuuint64_t>(std::max(rows, 1))};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(QSA_D) * 2, static_cast<cuuint64_t>(ld) * 2};
+  const cuuint32_t box[3] = {64u, 1u, static_cast<cuuint32_t>(box_rows)};
+  const cuuint32_t estr[3] = {1u, 1u, 1u};
+  const CUresult cr = encode(map, dtype == QSA_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                             3, const_cast<void*>(p), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (cr != CUDA_SUCCESS) return fail(QSA_ERR_CUDA, "tensor map of %s: error %d", name, static_cast<int>(cr));
+  return QSA_OK;
+}
+
+template <typename T>
+cudaError_t launch_prompt(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const qsa::FaArgs& a,
+                          int tiles, cudaStream_t s) {
+  auto kernel = qsa::prompt_attn_kernel<T>;
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (!(done.load(std::memory_order_relaxed) & bit)) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, qsa::kFaSmemBytes);
+    if (e != cudaSuccess) return e;
+    done.fetch_or(bit, std::memory_order_relaxed);
+  }
+  return launch_pdl(kernel, dim3(tiles * a.hq), dim3(qsa::kFaThreads), qsa::kFaSmemBytes, s, q, k, v, a);
+}
+
 }  // namespace
 
 extern "C" {
@@ -248,6 +284,60 @@ int qsa_paged_decode(const qsa_paged_cache* cache, const qsa_batch* batch, int r
       : dtype == QSA_F16 ? launch_decode<__half>(a, p, hq, s)
                          : launch_decode<__nv_bfloat16>(a, p, hq, s);
   if (r) return r;
+  return ok();
+}
+
+int qsa_prompt_attn(int nseq, const int32_t* cu_q, const int32_t* cu_k, int rows_q, int rows_k, int dtype, int hq,
+                    int hkv, const void* q, int64_t ldq, const void* k, int64_t ldk, const void* v, int64_t ldv,
+                    const void* gate, int64_t ldg, float scale, void* out, int64_t ldo, void* stream) {
+  int r;
+  if (dtype != QSA_F16 && dtype != QSA_BF16)
+    return fail(QSA_ERR_ARG, "dtype = %d: prompt attention takes QSA_F16 or QSA_BF16 rows", dtype);
+  if (hkv < 1 || hkv > QSA_MAX_HEADS || hq < 1 || hq > QSA_MAX_HEADS || hq % hkv)
+    return fail(QSA_ERR_ARG, "hq = %d must be a multiple of hkv = %d, both in [1, %d]", hq, hkv, QSA_MAX_HEADS);
+  if (nseq < 1 || nseq > QSA_MAX_ROWS) return fail(QSA_ERR_ARG, "nseq = %d out of [1, %d]", nseq, QSA_MAX_ROWS);
+  if (rows_q < 0 || rows_q > QSA_MAX_PACKED || rows_k < 0 || rows_k > QSA_MAX_PACKED)
+    return fail(QSA_ERR_ARG, "rows_q = %d, rows_k = %d out of [0, %d]", rows_q, rows_k, QSA_MAX_PACKED);
+  if (!cu_q || !cu_k) return fail(QSA_ERR_ARG, "cu_q and cu_k must not be NULL");
+  if (rows_q == 0) return ok();
+  if ((r = check_rows("q", q, ldq, hq, dtype)) || (r = check_rows("out", out, ldo, hq, dtype)) ||
+      (gate && (r = check_rows("gate", gate, ldg, hq, dtype))))
+    return r;
+  if (rows_k == 0) {  // nothing is read; the maps need some address
+    k = v = q;
+    ldk = ldv = ldq;
+  } else if ((r = check_rows("k", k, ldk, hkv, dtype)) || (r = check_rows("v", v, ldv, hkv, dtype))) {
+    return r;
+  }
+  if ((r = prepare_device())) return r;
+  PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
+  if ((r = tensor_map_encoder(&encode))) return r;
+  CUtensorMap tq, tk, tv;
+  if ((r = encode_rows(encode, &tq, "q", q, dtype, rows_q, hq, ldq, qsa::kFaM)) ||
+      (r = encode_rows(encode, &tk, "k", k, dtype, rows_k, hkv, ldk, qsa::kFaN)) ||
+      (r = encode_rows(encode, &tv, "v", v, dtype, rows_k, hkv, ldv, 64)))
+    return r;
+  qsa::FaArgs a;
+  a.cu_q = cu_q;
+  a.cu_k = cu_k;
+  a.nseq = nseq;
+  a.rows_q = rows_q;
+  a.rows_k = rows_k;
+  a.hq = hq;
+  a.group = hq / hkv;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.gate = gate;
+  a.out = out;
+  a.ldg = ldg;
+  a.ldo = ldo;
+  a.status = device_status();
+  // every sequence but its last tile is full, so this many tiles at most
+  const int64_t tiles = rows_q / qsa::kFaM + std::min(nseq, rows_q);
+  if (tiles * hq >= (static_cast<int64_t>(1) << 31)) return fail(QSA_ERR_ARG, "rows_q = %d x hq = %d out of range", rows_q, hq);
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = dtype == QSA_F16 ? launch_prompt<__half>(tq, tk, tv, a, static_cast<int>(tiles), s)
+                                         : launch_prompt<__nv_bfloat16>(tq, tk, tv, a, static_cast<int>(tiles), s);
+  if ((r = launched("prompt_attn_kernel", e))) return r;
   return ok();
 }
 

@@ -367,7 +367,7 @@ __global__ void __launch_bounds__(32 * MT * C, MINB) paged_decode_kernel(PdArgs 
       if (__any_sync(0xffffffffu, mx[0] > m_run[0] + kAttnShift || mx[1] > m_run[1] + kAttnShift)) {
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          const float mnew = fmaxf(m_run[r], mx[r]);
+          const float mnew = mx[r] > m_run[r] + kAttnShift ? mx[r] : m_run[r];
           const float alpha = attn_exp2(m_run[r] - mnew);
           l_run[r] *= alpha;
           m_run[r] = mnew;

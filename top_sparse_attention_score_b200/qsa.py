@@ -44,6 +44,8 @@ SIGNATURES = {
     "qsa_paged_read": (_I, [_P, _P, _I, _I, _P, _I64, _P, _I64, _P]),
     "qsa_paged_decode_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I]),
     "qsa_paged_decode": (_I, [_P, _P, _I, _I, _I, _I, _I, _P, _I64, _P, _I64, _F, _P, _SZ, _P, _I64, _P]),
+    "qsa_prompt_attn": (_I, [_I, _P, _P, _I, _I, _I, _I, _I, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _F, _P, _I64,
+                             _P]),
     "qsa_device_status": (_I, [_P, _P]),
     "qsa_selftest_wait_timeout": (_I, [_P]),
     "qsa_trace_begin": (_I, [_I, _P]),
@@ -470,6 +472,38 @@ def paged_decode(cache: PagedCache, batch: Batch, q, scale: float = 1 / 16, max_
             raise ValueError(f"ws must be contiguous on {dev}")
         _check(lib.qsa_paged_decode(cache._ref, batch._ref, rows, max_q, max_len, code, hq, qp, ldq, gp, ldg, scale,
                                     ws.data_ptr(), ws.numel() * ws.element_size(), op, ldo, _stream(stream)))
+    return out
+
+
+def prompt_attn(q, k, v, cu_q, cu_k=None, scale: float = 1 / 16, gate=None, out=None, stream=None):
+    """Causal attention over packed prompts: q, gate, out [rows][hq][256], k, v [keys][hkv][256]
+    (float16 or bfloat16, row strides free), cu_q / cu_k int32 [nseq + 1] (cu_k None: cu_q).
+    Rows of no sequence are left as they were (undefined in an output allocated here)."""
+    if cu_k is None:
+        cu_k = cu_q
+    _dev(cu_q, torch.int32, "cu_q")
+    _dev(cu_k, torch.int32, "cu_k")
+    if cu_q.dim() != 1 or cu_q.shape != cu_k.shape or cu_q.shape[0] < 2:
+        raise ValueError(f"cu_q and cu_k must be [nseq + 1], got {tuple(cu_q.shape)}, {tuple(cu_k.shape)}")
+    dev, dtype = q.device, q.dtype
+    if cu_q.device != dev or cu_k.device != dev:
+        raise ValueError(f"cu_q and cu_k must be on {dev}")
+    code = _dtype_code(dtype)
+    rows, hq, hkv = q.shape[0], q.shape[1], k.shape[1]
+    qp, ldq = _packed(q, hq, dtype, dev, "q")
+    kp, ldk = _packed(k, hkv, dtype, dev, "k")
+    vp, ldv = _packed(v, hkv, dtype, dev, "v")
+    _same_rows(v, k.shape[0], "v")
+    gp, ldg = (None, 0) if gate is None else _packed(gate, hq, dtype, dev, "gate")
+    if gate is not None:
+        _same_rows(gate, rows, "gate")
+    with _On(dev, stream):
+        if out is None:
+            out = torch.empty(rows, hq, D, dtype=dtype, device=dev)
+        op, ldo = _packed(out, hq, dtype, dev, "out")
+        _same_rows(out, rows, "out")
+        _check(load().qsa_prompt_attn(cu_q.shape[0] - 1, cu_q.data_ptr(), cu_k.data_ptr(), rows, k.shape[0], code, hq,
+                                      hkv, qp, ldq, kp, ldk, vp, ldv, gp, ldg, scale, op, ldo, _stream(stream)))
     return out
 
 
