@@ -183,7 +183,7 @@ int encode_rows(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap* map, cons
 
 template <typename T>
 cudaError_t launch_prompt(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const qsa::FaArgs& a,
-                          int tiles, cudaStream_t s) {
+                          int pairs, cudaStream_t s) {
   auto kernel = qsa::prompt_attn_kernel<T>;
   static std::atomic<uint64_t> done{0};
   int dev = 0;
@@ -195,7 +195,7 @@ cudaError_t launch_prompt(const CUtensorMap& q, const CUtensorMap& k, const CUte
     if (e != cudaSuccess) return e;
     done.fetch_or(bit, std::memory_order_relaxed);
   }
-  return launch_pdl(kernel, dim3(tiles * a.hq), dim3(qsa::kFaThreads), qsa::kFaSmemBytes, s, q, k, v, a);
+  return launch_pdl(kernel, dim3(2 * pairs), dim3(qsa::kFaThreads), qsa::kFaSmemBytes, s, q, k, v, a);
 }
 
 }  // namespace
@@ -314,8 +314,8 @@ int qsa_prompt_attn(int nseq, const int32_t* cu_q, const int32_t* cu_k, int rows
   if ((r = tensor_map_encoder(&encode))) return r;
   CUtensorMap tq, tk, tv;
   if ((r = encode_rows(encode, &tq, "q", q, dtype, rows_q, hq, ldq, qsa::kFaM)) ||
-      (r = encode_rows(encode, &tk, "k", k, dtype, rows_k, hkv, ldk, qsa::kFaN)) ||
-      (r = encode_rows(encode, &tv, "v", v, dtype, rows_k, hkv, ldv, 64)))
+      (r = encode_rows(encode, &tk, "k", k, dtype, rows_k, hkv, ldk, qsa::kFaN / 2)) ||
+      (r = encode_rows(encode, &tv, "v", v, dtype, rows_k, hkv, ldv, qsa::kFaN)))
     return r;
   qsa::FaArgs a;
   a.cu_q = cu_q;
@@ -331,12 +331,16 @@ int qsa_prompt_attn(int nseq, const int32_t* cu_q, const int32_t* cu_k, int rows
   a.ldg = ldg;
   a.ldo = ldo;
   a.status = device_status();
-  // every sequence but its last tile is full, so this many tiles at most
-  const int64_t tiles = rows_q / qsa::kFaM + std::min(nseq, rows_q);
-  if (tiles * hq >= (static_cast<int64_t>(1) << 31)) return fail(QSA_ERR_ARG, "rows_q = %d x hq = %d out of range", rows_q, hq);
+  // A pair of CTAs takes two heads of a KV head where their number is even: both then see the
+  // same keys, while two row blocks of one head differ by a tile.
+  a.by_heads = a.group % 2 == 0;
+  const int block_rows = a.by_heads ? qsa::kFaM : 2 * qsa::kFaM, sets = a.by_heads ? hq / 2 : hq;
+  // every block of a sequence but its last is full, so there are at most this many
+  const int64_t pairs = (static_cast<int64_t>(rows_q) / block_rows + std::min(nseq, rows_q)) * sets;
+  if (pairs >= (static_cast<int64_t>(1) << 30)) return fail(QSA_ERR_ARG, "rows_q = %d x hq = %d out of range", rows_q, hq);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = dtype == QSA_F16 ? launch_prompt<__half>(tq, tk, tv, a, static_cast<int>(tiles), s)
-                                         : launch_prompt<__nv_bfloat16>(tq, tk, tv, a, static_cast<int>(tiles), s);
+  const cudaError_t e = dtype == QSA_F16 ? launch_prompt<__half>(tq, tk, tv, a, static_cast<int>(pairs), s)
+                                         : launch_prompt<__nv_bfloat16>(tq, tk, tv, a, static_cast<int>(pairs), s);
   if ((r = launched("prompt_attn_kernel", e))) return r;
   return ok();
 }

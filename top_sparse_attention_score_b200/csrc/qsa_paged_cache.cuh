@@ -112,9 +112,11 @@ struct Row8<__half> {
       x[2 * i + 1] = f.y;
     }
   }
+  static __device__ __forceinline__ uint4 pack(const float (&x)[8]) {
+    return make_uint4(pack_half2(x[0], x[1]), pack_half2(x[2], x[3]), pack_half2(x[4], x[5]), pack_half2(x[6], x[7]));
+  }
   static __device__ __forceinline__ void store(__half* p, const float (&x)[8]) {
-    *reinterpret_cast<uint4*>(p) = make_uint4(pack_half2(x[0], x[1]), pack_half2(x[2], x[3]),
-                                              pack_half2(x[4], x[5]), pack_half2(x[6], x[7]));
+    *reinterpret_cast<uint4*>(p) = pack(x);
   }
 };
 
@@ -135,9 +137,11 @@ struct Row8<__nv_bfloat16> {
       x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
     }
   }
+  static __device__ __forceinline__ uint4 pack(const float (&x)[8]) {
+    return make_uint4(pack_bf162(x[0], x[1]), pack_bf162(x[2], x[3]), pack_bf162(x[4], x[5]), pack_bf162(x[6], x[7]));
+  }
   static __device__ __forceinline__ void store(__nv_bfloat16* p, const float (&x)[8]) {
-    *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf162(x[0], x[1]), pack_bf162(x[2], x[3]),
-                                              pack_bf162(x[4], x[5]), pack_bf162(x[6], x[7]));
+    *reinterpret_cast<uint4*>(p) = pack(x);
   }
 };
 

@@ -4,15 +4,24 @@
 //   O_i = sum_{j <= i + m - n} exp(x_ij - M_i) V_j / sum_j exp(x_ij - M_i),  x_ij = scale * q_i . k_j,
 // in one pass over the keys with a running reference maximum M and sum; both are fp32.
 //
-// One CTA computes 128 rows of one head:
-//   * Q (128 x 256) stays in shared memory; K and V tiles of 128 keys stream through a ring of
-//     five 32 KB slots (half a tile each) that one thread fills by TMA;
-//   * one thread issues the tcgen05.mma: S_i = Q K_i^T into one of two 128-column TMEM buffers
-//     (so S_{i+1} is computed while the softmax works on S_i), then O += P_i V_i with P_i read
-//     from TMEM (the weights overwrite their scores as 16-bit pairs) and V_i as an MN-major
-//     operand.  2 x 128 columns of S and 256 of O fill the 512 of TMEM;
-//   * four softmax warps own a row per thread: no exchange between threads.  The reference
-//     maximum moves only when a tile exceeds it by more than 2^8, so O is rarely rescaled.
+// Two CTAs on neighbouring SMs (a cluster) work as one: tcgen05.mma with cta_group::2 multiplies
+// 256 query rows -- 128 rows of two heads of a KV head, or 256 rows of one head where the heads
+// per KV head are odd -- by keys of which each CTA holds half.  At head dim 256 that is what the
+// tensor cores need: a single CTA's product of 128 rows reads as much shared memory as the
+// tensor cores take time (8 KB per 64 cycles, with the loads' writes on top), and every SM would
+// fetch all of K and V; a pair halves both.  Per CTA:
+//   * Q (128 x 256) stays in shared memory; tiles of 128 keys stream through a ring of five
+//     32 KB slots that one thread fills by TMA: of K its 64 keys, of V its 128 dims;
+//   * the leader CTA's MMA thread issues S_i = Q K_i^T into one of two 128-column TMEM buffers,
+//     then O += P_i V_i with P_i read from TMEM (the weights overwrite their scores as 16-bit
+//     pairs) and V_i as an MN-major operand.  2 x 128 columns of S and 256 of O fill TMEM;
+//   * two softmax warpgroups take the key tiles in turn, a thread a row, so one exchanges nothing
+//     but the row's reference maximum with the other, and the exponentials of one overlap the
+//     TMEM traffic of the other.  The reference moves only when a tile exceeds it by more than
+//     2^8, so O is rarely rescaled.  At a tile's end each reads half of O out (divide, gate,
+//     store) while the next tile's scores are computed;
+//   * the grid has a pair per query tile; a running pair takes over one that has not started
+//     through cluster launch control, so the next tile's loads overlap the end of this one.
 //
 // The weights are rounded to the input type for the tensor cores (fp16: 2^-12, bf16: 2^-9 relative, as
 // the output is); the sum is over the unrounded weights in fp32.
@@ -28,21 +37,49 @@ namespace qsa {
 constexpr int kFaM = 128;      // query rows of a CTA
 constexpr int kFaN = 128;      // keys of a tile
 constexpr int kFaSlots = 5;
-constexpr int kFaSlotBytes = 32 * 1024;  // half a K or V tile
+constexpr int kFaSlotBytes = 32 * 1024;  // a CTA's half of a K or V tile
 constexpr int kFaQBytes = kFaM * kD * 2;
-constexpr int kFaThreads = 192;  // four softmax warps, TMA, MMA
+// Three warpgroups: two of softmax; TMA, MMA and two idle warps.  The softmax holds a row's 128
+// scores in registers, so it takes some from the others.
+constexpr int kFaThreads = 384;
+constexpr int kFaRegsLaunch = 168;  // what 384 threads of one CTA per SM get
+constexpr int kFaRegsSoftmax = 216, kFaRegsIssue = 72;
+static_assert(2 * kFaRegsSoftmax + kFaRegsIssue <= 3 * kFaRegsLaunch, "registers of the launch");
+// growing to fewer, or shrinking to more, than the launch's is an illegal instruction
+static_assert(kFaRegsSoftmax > kFaRegsLaunch && kFaRegsIssue < kFaRegsLaunch, "which groups grow and which shrink");
 constexpr float kFaShift = 8.f;
 constexpr float kFaNoMax = -1.0e30f;
 
-struct __align__(8) FaBarriers {
-  uint64_t full[kFaSlots];
+// What a pair computes, and a CTA's part of it.
+struct FaTile {
+  int live;        // 0: no more tiles
+  int row0, rows;  // this CTA's first packed query row; its rows (<= 0: none)
+  int key0, keys;  // first packed key row; keys that any row of the pair sees
+  int seen0;       // keys that this CTA's first row sees (row r sees seen0 + r)
+  int head;
+};
+
+// (L): only the leader CTA's is used, by both CTAs.
+struct __align__(16) FaBarriers {
+  uint4 next;                    // answer of the launch control
+  uint64_t next_full;
+  uint64_t next_free;            // (L) the peer has read the answer
+  uint64_t full[kFaSlots];       // (L) both CTAs' halves have landed
   uint64_t empty[kFaSlots];
-  uint64_t q_full;
+  uint64_t q_full;               // (L)
+  uint64_t q_empty;
   uint64_t s_full[2];
-  uint64_t p_ready[2];
-  uint64_t pv_done;
-  uint64_t tail;
-  uint64_t drain;
+  uint64_t p_ready[2];           // (L) four warps of each CTA
+  uint64_t pv_done;              // one phase per key tile
+  uint64_t o_full;               // one phase per query tile: O complete
+  uint64_t o_free;               // (L) read out: eight warps of each CTA
+  uint64_t tile_full[2], tile_empty[2];
+  uint64_t tail, drain;
+  FaTile tile[2];
+  uint64_t m_full[2][4];         // a group's warp has passed its rows' reference maxima
+  uint64_t l_full[4], l_free[4]; // both groups' sums of a warp's rows are there; were read
+  float m_ref[kFaM];             // the rows' reference maxima, passed between the warpgroups
+  float l_part[2][kFaM];
   uint32_t tmem_base;
   uint32_t abort;
 };
@@ -55,6 +92,7 @@ struct FaArgs {
   int nseq;
   int rows_q, rows_k;
   int hq, group;
+  int by_heads;  // a pair is two heads (else two blocks of rows)
   float scale_log2;
   const void* gate;
   void* out;
@@ -87,14 +125,105 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
 
-// D (TMEM) (+)= A (TMEM) . B (shared memory)
-__device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
-                                            uint32_t accumulate) {
+template <int N>
+__device__ __forceinline__ void regs_grow() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void regs_shrink() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N)); }
+
+// ---- a pair of CTAs
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;\n" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync_all() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+}
+// The cluster address of a shared-memory object of the leader CTA (rank 0).
+__device__ __forceinline__ uint32_t leader_addr(const void* p) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;\n" : "=r"(a) : "r"(smem_u32(p)));
+  return a;
+}
+// Arrivals at a barrier of either CTA.  They carry no generic memory between the CTAs (TMA bytes
+// count on the barrier themselves, TMEM is ordered by the tcgen05 fences), so they are not
+// cluster-scope releases: those wait for all of the thread's memory, 800 cycles each here.
+__device__ __forceinline__ void mbar_arrive_at(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];\n" ::"r"(cluster_addr) : "memory");
+}
+__device__ __forceinline__ void mbar_expect_tx_at(uint32_t cluster_addr, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cluster.b64 _, [%0], %1;\n" ::"r"(cluster_addr),
+               "r"(bytes)
+               : "memory");
+}
+// A load into this CTA's shared memory whose bytes complete a barrier of either CTA of the pair.
+__device__ __forceinline__ void tma_load_3d_pair(void* dst, const CUtensorMap* map, int x, int y, int z,
+                                                 uint32_t bar_cluster_addr) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, "
+      "%4}], [%5];\n" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar_cluster_addr)
+      : "memory");
+}
+__device__ __forceinline__ void umma2_f16_ss(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                             uint32_t accumulate) {
   asm volatile(
       "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
+      " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void umma2_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                             uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
       "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
+}
+// The barrier at this offset of both CTAs completes when the MMAs issued so far have finished.
+__device__ __forceinline__ void umma2_commit(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n" ::"r"(
+          smem_u32(bar)),
+      "h"(static_cast<uint16_t>(3))
+      : "memory");
+}
+__device__ __forceinline__ void tmem2_alloc(uint32_t* dst_smem, uint32_t cols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(smem_u32(dst_smem)),
+               "r"(cols));
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;\n" ::);
+}
+__device__ __forceinline__ void tmem2_dealloc(uint32_t base, uint32_t cols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;\n" ::"r"(base), "r"(cols));
+}
+
+// Bounded wait by try_wait: the thread sleeps in hardware until the phase completes or a short
+// limit of the hardware's passes, so waiting takes few issue slots from the warps that work; the
+// clock (a read of %globaltimer is slow) and the abort flag are read only when it returns
+// without the phase.
+__device__ __forceinline__ bool fa_wait(uint64_t* bar, uint32_t parity, uint32_t* abort, uint32_t* status) {
+  const uint32_t addr = smem_u32(bar);
+  unsigned long long t0 = 0ull;
+  for (;;) {
+    uint32_t done;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+        " selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(done)
+        : "r"(addr), "r"(parity)
+        : "memory");
+    if (done) return true;
+    if (*reinterpret_cast<volatile uint32_t*>(abort)) return false;
+    const unsigned long long now = global_ns();
+    if (t0 == 0ull) t0 = now;
+    if (now - t0 > kWaitLimitNs) {
+      atomicExch(status, kStatusTimeout);
+      *reinterpret_cast<volatile uint32_t*>(abort) = 1u;
+      return false;
+    }
+  }
 }
 
 // MN-major operand with the 128-byte swizzle: rows of 64 MN elements (128 bytes), 8-row atoms
@@ -107,31 +236,55 @@ __device__ __forceinline__ uint64_t umma_desc_mn_sw128(uint32_t saddr, uint32_t 
 // kind::f16 instruction descriptor with both operands bf16 instead of fp16.
 constexpr uint32_t kUmmaBf16 = (1u << 7) | (1u << 10);
 
-// The sequence and 128-row block of flat tile `idx`, the last tile first (a sequence's last
-// block sees the most keys, so the longest work starts first).  Every warp computes the same.
-struct FaTile {
-  int row0, rows;  // first packed query row of the tile; its rows (<= 0: no such tile)
-  int key0, keys;  // first packed key row; keys that any row of the tile sees
-  int seen0;       // keys that the tile's first row sees (row r sees seen0 + r)
-};
+// Cluster launch control: ask for a pair of this grid that has not started; the 16-byte answer
+// goes to this offset of both CTAs and completes their `bar`.
+__device__ __forceinline__ void clc_request(uint4* answer, uint64_t* bar) {
+  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.multicast::cluster::all.b128 "
+      "[%0], [%1];\n" ::"r"(
+                   smem_u32(answer)),
+               "r"(smem_u32(bar))
+               : "memory");
+}
+
+// The x index of the pair's first CTA, -1 when none was left.
+__device__ __forceinline__ int clc_answer(const uint4* answer) {
+  uint32_t got, x;
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b128 r;\n ld.shared.b128 r, [%2];\n"
+      " clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n selp.u32 %0, 1, 0, p;\n mov.u32 %1, 0;\n"
+      " @p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r;\n}\n"
+      : "=r"(got), "=r"(x)
+      : "r"(smem_u32(answer))
+      : "memory");
+  return got ? static_cast<int>(x) : -1;
+}
 
 __device__ __forceinline__ int fa_bound(const int* cu, int s, int rows) { return min(max(__ldg(cu + s), 0), rows); }
 
-__device__ __forceinline__ FaTile fa_tile(const FaArgs& a, int idx) {
+// Row blocks of sequence s.
+__device__ __forceinline__ int fa_blocks(const FaArgs& a, int s, int block_rows) {
+  if (s >= a.nseq) return 0;
+  const int n = fa_bound(a.cu_q, s + 1, a.rows_q) - fa_bound(a.cu_q, s, a.rows_q);
+  return (max(0, n) + block_rows - 1) / block_rows;
+}
+
+// The part of CTA `rank` of pair `pair` of the grid: heads fastest (they share K and V through
+// L2), then row blocks, the last first (a sequence's last block sees the most keys, so the
+// longest work starts first).  The warp computes it together.
+__device__ __forceinline__ FaTile fa_tile(const FaArgs& a, int pair, int rank) {
   const int lane = threadIdx.x & 31;
-  FaTile t = {0, 0, 0, 0, 0};
+  const int sets = a.by_heads ? a.hq / 2 : a.hq, block_rows = a.by_heads ? kFaM : 2 * kFaM;
+  const int idx = pair / sets;
+  FaTile t = {0, 0, 0, 0, 0, 0, 0};
+  t.head = a.by_heads ? 2 * (pair % sets) + rank : pair % sets;
   int total = 0;
-  for (int s0 = 0; s0 < a.nseq; s0 += 32) {
-    const int s = s0 + lane;
-    if (s < a.nseq) total += (max(0, fa_bound(a.cu_q, s + 1, a.rows_q) - fa_bound(a.cu_q, s, a.rows_q)) + kFaM - 1) / kFaM;
-  }
+  for (int s0 = 0; s0 < a.nseq; s0 += 32) total += fa_blocks(a, s0 + lane, block_rows);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
   if (idx >= total) return t;
   const int want = total - 1 - idx;
   for (int s0 = 0, base = 0; s0 < a.nseq; s0 += 32) {
-    const int s = s0 + lane;
-    const int nb = s < a.nseq ? (max(0, fa_bound(a.cu_q, s + 1, a.rows_q) - fa_bound(a.cu_q, s, a.rows_q)) + kFaM - 1) / kFaM : 0;
+    const int nb = fa_blocks(a, s0 + lane, block_rows);
     int inc = nb;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -144,11 +297,13 @@ __device__ __forceinline__ FaTile fa_tile(const FaArgs& a, int idx) {
       const int seq = s0 + l, block = want - base - __shfl_sync(0xffffffffu, inc - nb, l);
       const int q0 = fa_bound(a.cu_q, seq, a.rows_q), n = fa_bound(a.cu_q, seq + 1, a.rows_q) - q0;
       const int k0 = fa_bound(a.cu_k, seq, a.rows_k), m = max(0, fa_bound(a.cu_k, seq + 1, a.rows_k) - k0);
-      t.row0 = q0 + block * kFaM;
-      t.rows = min(kFaM, n - block * kFaM);
+      const int first = block * block_rows, off = a.by_heads ? 0 : rank * kFaM;
+      t.live = 1;
+      t.row0 = q0 + first + off;
+      t.rows = min(kFaM, n - first - off);
       t.key0 = k0;
-      t.seen0 = block * kFaM + 1 + m - n;
-      t.keys = max(0, min(m, t.seen0 + t.rows - 1));
+      t.seen0 = first + off + 1 + m - n;
+      t.keys = max(0, min(m, m - n + min(n, first + block_rows)));
       return t;
     }
     base += __shfl_sync(0xffffffffu, inc, 31);
@@ -156,15 +311,15 @@ __device__ __forceinline__ FaTile fa_tile(const FaArgs& a, int idx) {
   return t;
 }
 
-// grid: hq * (upper bound of the tiles), heads fastest (the heads of a KV head share its K and
-// V through L2); block: 192; dynamic shared memory: kFaSmemBytes.
+// grid: 2 * pairs (head sets * an upper bound of the row blocks), clusters of 2; block: 384;
+// dynamic shared memory: kFaSmemBytes.
 template <typename T>
-__global__ void __launch_bounds__(kFaThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFaThreads, 1)
     prompt_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
                        const __grid_constant__ CUtensorMap tmap_v, FaArgs a) {
-  constexpr uint32_t kType = sizeof(T) == 2 && std::is_same<T, __nv_bfloat16>::value ? kUmmaBf16 : 0u;
-  constexpr uint32_t kIdescQK = umma_idesc_f16(kFaM, kFaN, false, false) | kType;
-  constexpr uint32_t kIdescPV = umma_idesc_f16(kFaM, kD, false, true) | kType;
+  constexpr uint32_t kType = std::is_same<T, __nv_bfloat16>::value ? kUmmaBf16 : 0u;
+  constexpr uint32_t kIdescQK = umma_idesc_f16(2 * kFaM, kFaN, false, false) | kType;
+  constexpr uint32_t kIdescPV = umma_idesc_f16(2 * kFaM, kD, false, true) | kType;
   extern __shared__ unsigned char fsm_raw[];
   unsigned char* fsm =
       reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(fsm_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -172,267 +327,420 @@ __global__ void __launch_bounds__(kFaThreads, 1)
   unsigned char* ring = fsm + kFaQBytes;
   FaBarriers& fb = *reinterpret_cast<FaBarriers*>(ring + kFaSlots * kFaSlotBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int head = static_cast<int>(blockIdx.x) % a.hq, kvh = head / a.group;
+  const int rank = static_cast<int>(cluster_rank());
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, fa_wait(bar, parity, &fb.abort, a.status)) != 0;
+  };
 
   griddep_wait();
-  const FaTile tile = fa_tile(a, static_cast<int>(blockIdx.x) / a.hq);
-  if (tile.rows <= 0) return;
-  const int ntiles = (tile.keys + kFaN - 1) / kFaN;
+  const FaTile first = fa_tile(a, static_cast<int>(blockIdx.x) / 2, rank);
+  if (!first.live) return;  // both CTAs of the pair
 
   if (threadIdx.x == 0) {
+    mbar_init(&fb.next_full, 1);
+    mbar_init(&fb.next_free, 1);
     for (int s = 0; s < kFaSlots; ++s) {
-      mbar_init(&fb.full[s], 1);
+      mbar_init(&fb.full[s], 2);
       mbar_init(&fb.empty[s], 1);
     }
-    mbar_init(&fb.q_full, 1);
+    mbar_init(&fb.q_full, 2);
+    mbar_init(&fb.q_empty, 1);
     for (int b = 0; b < 2; ++b) {
       mbar_init(&fb.s_full[b], 1);
-      mbar_init(&fb.p_ready[b], 4);
+      mbar_init(&fb.p_ready[b], 8);
+      mbar_init(&fb.tile_full[b], 1);
+      mbar_init(&fb.tile_empty[b], rank == 0 ? 9 : 8);  // eight softmax warps, the MMA thread
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&fb.m_full[0][i], 1);
+      mbar_init(&fb.m_full[1][i], 1);
+      mbar_init(&fb.l_full[i], 2);
+      mbar_init(&fb.l_free[i], 2);
     }
     mbar_init(&fb.pv_done, 1);
+    mbar_init(&fb.o_full, 1);
+    mbar_init(&fb.o_free, 16);
     mbar_init(&fb.tail, 1);
     mbar_init(&fb.drain, 1);
     fb.abort = 0u;
     mbar_init_fence();
   }
-  if (warp == 5) tmem_alloc(&fb.tmem_base, 512u);
+  if (warp == 9) tmem2_alloc(&fb.tmem_base, 512u);
   tc_fence_before();
   __syncthreads();
+  cluster_sync_all();
   tc_fence_after();
   const uint32_t tmem = fb.tmem_base;
   const uint32_t tmem_o = tmem + 2 * kFaN;
 
-  if (warp == 4) {
-    // ---------------- TMA: Q, then K_0, K_1, V_0, K_2, V_1, ...
-    bool ok = true;
-    if (lane == 0 && ntiles > 0) {
-      mbar_expect_tx(&fb.q_full, kFaQBytes);
-      for (int c = 0; c < 4; ++c) tma_load_3d(sq + c * (kFaM * 128), &tmap_q, 64 * c, head, tile.row0, &fb.q_full);
-    }
-    int n = 0;  // half tiles so far
-    auto acquire = [&](int& slot) {
-      slot = n % kFaSlots;
-      const uint32_t parity = ((n / kFaSlots) & 1) ^ 1;
-      ++n;
-      return mbar_wait_warp(&fb.empty[slot], parity, &fb.abort, a.status);
-    };
-    auto load_k = [&](int i) {
-      for (int h = 0; h < 2 && ok; ++h) {  // dims 128 h .. 128 h + 127 of 128 keys
+  if (warp >= 8) {
+    regs_shrink<kFaRegsIssue>();
+    if (warp == 8) {
+      // ---------------- tiles and TMA.  The tiles come in the order the MMA thread takes them:
+      // K_0, K_1, V_0, K_2, V_1, ..., and a query tile's last V behind the next one's K_0.
+      bool ok = true, asked = false;
+      int n = 0, tails = 0, loads_q = 0;  // K and V tiles, partial ones, Q tiles so far
+      auto acquire = [&](int& slot) {
+        slot = n % kFaSlots;
+        ok = wait(&fb.empty[slot], ((n / kFaSlots) & 1) ^ 1);
+        if (ok) ++n;
+        return ok;
+      };
+      auto load_k = [&](const FaTile& t, int i) {
         int slot;
-        ok = acquire(slot);
-        if (ok && lane == 0) {
-          mbar_expect_tx(&fb.full[slot], kFaSlotBytes);
-          for (int c = 0; c < 2; ++c)
-            tma_load_3d(ring + slot * kFaSlotBytes + c * (kFaN * 128), &tmap_k, 64 * (2 * h + c), kvh,
-                        tile.key0 + i * kFaN, &fb.full[slot]);
-        }
-      }
-    };
-    int tails = 0;
-    auto load_v = [&](int i) {
-      for (int h = 0; h < 2 && ok; ++h) {  // 64 keys, all dims
-        int slot;
-        ok = acquire(slot);
-        if (!ok) return;
-        unsigned char* dst = ring + slot * kFaSlotBytes;
-        const int first = i * kFaN + 64 * h, valid = tile.keys - first;
-        uint64_t* bar = valid >= 64 ? &fb.full[slot] : &fb.tail;
+        if (!acquire(slot)) return;
         if (lane == 0) {
-          mbar_expect_tx(bar, kFaSlotBytes);
-          for (int c = 0; c < 4; ++c) tma_load_3d(dst + c * (64 * 128), &tmap_v, 64 * c, kvh, tile.key0 + first, bar);
+          const uint32_t bar = leader_addr(&fb.full[slot]);
+          mbar_expect_tx_at(bar, kFaSlotBytes);
+          for (int c = 0; c < 4; ++c)
+            tma_load_3d_pair(ring + slot * kFaSlotBytes + c * (64 * 128), &tmap_k, 64 * c, t.head / a.group,
+                             t.key0 + i * kFaN + 64 * rank, bar);
         }
-        if (valid < 64) {
+      };
+      auto load_v = [&](const FaTile& t, int i) {
+        int slot;
+        if (!acquire(slot)) return;
+        unsigned char* dst = ring + slot * kFaSlotBytes;
+        const int valid = t.keys - i * kFaN;
+        const uint32_t full = leader_addr(&fb.full[slot]);
+        if (lane == 0) {
+          if (valid >= kFaN) mbar_expect_tx_at(full, kFaSlotBytes);
+          else mbar_expect_tx(&fb.tail, kFaSlotBytes);
+          for (int c = 0; c < 2; ++c) {
+            if (valid >= kFaN)
+              tma_load_3d_pair(dst + c * (kFaN * 128), &tmap_v, 128 * rank + 64 * c, t.head / a.group,
+                               t.key0 + i * kFaN, full);
+            else
+              tma_load_3d(dst + c * (kFaN * 128), &tmap_v, 128 * rank + 64 * c, t.head / a.group, t.key0 + i * kFaN,
+                          &fb.tail);
+          }
+        }
+        if (valid < kFaN) {
           // Rows behind the last key a row of this tile sees may be another sequence's, or
           // nobody's, and hold anything; a weight of 0 times NaN would spread, so they become 0.
-          ok = mbar_wait_warp(&fb.tail, tails++ & 1, &fb.abort, a.status);
-          if (!ok) return;
-          const int r0 = max(valid, 0);
-          for (int e = lane; e < (64 - r0) * 32; e += 32) {
-            const int r = r0 + (e >> 5), c = (e >> 3) & 3, part = e & 7;
-            *reinterpret_cast<uint4*>(dst + c * (64 * 128) + r * 128 + part * 16) = make_uint4(0u, 0u, 0u, 0u);
+          if (!(ok = wait(&fb.tail, tails++ & 1))) return;
+          for (int e = lane; e < (kFaN - valid) * 16; e += 32) {
+            const int r = valid + (e >> 4), c = (e >> 3) & 1, part = e & 7;
+            *reinterpret_cast<uint4*>(dst + c * (kFaN * 128) + r * 128 + part * 16) = make_uint4(0u, 0u, 0u, 0u);
           }
           fence_proxy_async_smem();
+          asm volatile("fence.acq_rel.cluster;\n" ::: "memory");  // these are generic writes
           __syncwarp();
-          if (lane == 0) mbar_arrive(&fb.full[slot]);
+          if (lane == 0) mbar_arrive_at(full);
         }
-      }
-    };
-    for (int i = 0; i < ntiles && ok; ++i) {
-      load_k(i);
-      if (i > 0 && ok) load_v(i - 1);
-    }
-    if (ntiles > 0 && ok) load_v(ntiles - 1);
-    if (!ok && lane == 0) {  // drain copies that may still be in flight before the CTA leaves
-      mbar_drain_wait(&fb.q_full, 0);
-      if (tails > 0) mbar_drain_wait(&fb.tail, (tails - 1) & 1);
-      for (int j = max(0, n - 1 - kFaSlots); j < n - 1; ++j) mbar_drain_wait(&fb.full[j % kFaSlots], (j / kFaSlots) & 1);
-    }
-    __syncwarp();
-  } else if (warp == 5) {
-    // ---------------- MMA
-    if (lane == 0 && ntiles > 0) {
-      int n = 0;
-      bool ok = mbar_wait(&fb.q_full, 0, &fb.abort, a.status);
-      const uint32_t q0 = smem_u32(sq), r0 = smem_u32(ring);
-      auto take = [&](int& slot) {
-        slot = n % kFaSlots;
-        const uint32_t parity = (n / kFaSlots) & 1;
-        ++n;
-        const bool got = mbar_wait(&fb.full[slot], parity, &fb.abort, a.status);
-        tc_fence_after();
-        return got;
       };
-      auto scores = [&](int i) {  // S_i = Q K_i^T
-        for (int h = 0; h < 2 && ok; ++h) {
-          int slot;
-          if (!(ok = take(slot))) return;
-#pragma unroll
-          for (int ks = 0; ks < 8; ++ks) {
-            const uint32_t off = (ks >> 2) * (kFaM * 128) + (ks & 3) * 32;
-            umma_f16(tmem + (i & 1) * kFaN, umma_desc_k_sw128(q0 + 2 * h * (kFaM * 128) + off, 1024),
-                     umma_desc_k_sw128(r0 + slot * kFaSlotBytes + off, 1024), kIdescQK, h + ks > 0 ? 1u : 0u);
+      FaTile tile = first, last;  // last: the tile whose last V is still to come
+      last.keys = 0;
+      for (int w = 0;; ++w) {
+        // hand the tile to the other roles
+        if (!(ok = wait(&fb.tile_empty[w & 1], ((w >> 1) & 1) ^ 1))) break;
+        if (lane == 0) {
+          fb.tile[w & 1] = tile;
+          mbar_arrive(&fb.tile_full[w & 1]);
+        }
+        if (tile.live) {
+          if (lane == 0) mbar_expect_tx(&fb.next_full, 16);
+          asked = true;
+          if (rank == 0) {  // the peer has read the answer before
+            if (w > 0 && !(ok = wait(&fb.next_free, (w - 1) & 1))) break;
+            if (lane == 0) clc_request(&fb.next, &fb.next_full);
           }
-          umma_commit(&fb.empty[slot]);
         }
-        umma_commit(&fb.s_full[i & 1]);
-      };
-      if (ok) scores(0);
-      for (int i = 0; i < ntiles && ok; ++i) {
-        // S_{i+1} takes the buffer of P_{i-1}, which the product issued before has read
-        if (i + 1 < ntiles) scores(i + 1);
-        if (!ok || !(ok = mbar_wait(&fb.p_ready[i & 1], (i >> 1) & 1, &fb.abort, a.status))) break;
-        tc_fence_after();
-        for (int h = 0; h < 2 && ok; ++h) {  // O += P_i V_i
+        const int ntiles = tile.live ? (tile.keys + kFaN - 1) / kFaN : 0;
+        if (ntiles > 0) {
+          if (!(ok = wait(&fb.q_empty, (loads_q & 1) ^ 1))) break;
+          ++loads_q;
+          if (lane == 0) {
+            const uint32_t bar = leader_addr(&fb.q_full);
+            mbar_expect_tx_at(bar, kFaQBytes);
+            for (int c = 0; c < 4; ++c)
+              tma_load_3d_pair(sq + c * (kFaM * 128), &tmap_q, 64 * c, tile.head, tile.row0, bar);
+          }
+          load_k(tile, 0);
+        }
+        if (ok && last.keys > 0) load_v(last, (last.keys - 1) / kFaN);
+        last.keys = 0;
+        if (!ok || !tile.live) break;
+        // the next tile is looked up behind K_1: before this tile's last V, which follows the
+        // next tile's K_0, is due
+        FaTile next = tile;
+        for (int i = 1; i < max(ntiles, 2) && ok; ++i) {
+          if (i < ntiles) load_k(tile, i);
+          if (ok && i == 1) {
+            if (!(ok = wait(&fb.next_full, w & 1))) break;
+            asked = false;
+            const int got = clc_answer(&fb.next);
+            fence_proxy_async_smem();  // the answer has been read before the next one may be written
+            __syncwarp();
+            if (rank == 1 && lane == 0) mbar_arrive_at(leader_addr(&fb.next_free));
+            next.live = 0;
+            if (got >= 0) next = fa_tile(a, got / 2, rank);
+          }
+          if (ok && i < ntiles) load_v(tile, i - 1);
+        }
+        if (!ok) break;
+        if (ntiles > 0) last = tile;
+        tile = next;
+      }
+      if (!ok && lane == 0) {  // give copies that may still be in flight time before the CTA leaves
+        if (asked) mbar_drain_wait(&fb.next_full, 0), mbar_drain_wait(&fb.next_full, 1);
+        if (tails > 0) mbar_drain_wait(&fb.tail, (tails - 1) & 1);
+        if (rank == 0) {
+          if (loads_q > 0) mbar_drain_wait(&fb.q_full, (loads_q - 1) & 1);
+          for (int j = max(0, n - kFaSlots); j < n; ++j) mbar_drain_wait(&fb.full[j % kFaSlots], (j / kFaSlots) & 1);
+        }
+      }
+      __syncwarp();
+    } else if (warp == 9 && rank == 0) {
+      // ---------------- MMA, for both CTAs.  The product O += P_j V_j of step j is issued after
+      // the scores of step j + 1, across query tiles too.
+      if (lane == 0) {
+        bool ok = true;
+        int n = 0;     // K and V tiles so far
+        int step = 0;  // key tiles whose scores were issued, over all query tiles
+        int q_tiles = 0;
+        const uint32_t q0 = smem_u32(sq), r0 = smem_u32(ring);
+        auto wait1 = [&](uint64_t* bar, uint32_t parity) { return ok = fa_wait(bar, parity, &fb.abort, a.status); };
+        auto take = [&](int& slot) {
+          slot = n % kFaSlots;
+          wait1(&fb.full[slot], (n / kFaSlots) & 1);
+          ++n;
+          tc_fence_after();
+          return ok;
+        };
+        auto scores = [&]() {  // S = Q K_step^T
+          const int b = step & 1;
           int slot;
-          if (!(ok = take(slot))) break;
+          if (!take(slot)) return;
 #pragma unroll
-          for (int ks = 0; ks < 4; ++ks)
-            umma_f16_ts(tmem_o, tmem + (i & 1) * kFaN + (h * 4 + ks) * 8,
-                        umma_desc_mn_sw128(r0 + slot * kFaSlotBytes + ks * 2048, 64 * 128, 1024), kIdescPV,
-                        i + h + ks > 0 ? 1u : 0u);
-          umma_commit(&fb.empty[slot]);
+          for (int ks = 0; ks < 16; ++ks)
+            umma2_f16_ss(tmem + b * kFaN, umma_desc_k_sw128(q0 + (ks >> 2) * (kFaM * 128) + (ks & 3) * 32, 1024),
+                         umma_desc_k_sw128(r0 + slot * kFaSlotBytes + (ks >> 2) * (64 * 128) + (ks & 3) * 32, 1024),
+                         kIdescQK, ks > 0 ? 1u : 0u);
+          umma2_commit(&fb.empty[slot]);
+          umma2_commit(&fb.s_full[b]);
+          ++step;
+        };
+        auto product = [&](int j, bool fresh) {  // O (+)= P_j V_j
+          const int b = j & 1;
+          int slot;
+          if (!wait1(&fb.p_ready[b], (j >> 1) & 1) || !take(slot)) return;
+#pragma unroll
+          for (int ks = 0; ks < 8; ++ks)
+            umma2_f16_ts(tmem_o, tmem + b * kFaN + ks * 8,
+                         umma_desc_mn_sw128(r0 + slot * kFaSlotBytes + ks * 2048, kFaN * 128, 1024), kIdescPV,
+                         fresh && ks == 0 ? 0u : 1u);
+          umma2_commit(&fb.empty[slot]);
+          umma2_commit(&fb.pv_done);
+        };
+        auto tile_steps = [&](int w) {  // key tiles of query tile w; -1: no more tiles
+          if (!wait1(&fb.tile_full[w & 1], (w >> 1) & 1)) return -1;
+          const int live = fb.tile[w & 1].live, keys = fb.tile[w & 1].keys;
+          mbar_arrive(&fb.tile_empty[w & 1]);
+          return live ? (keys + kFaN - 1) / kFaN : -1;
+        };
+        auto open_tile = [&]() {  // its Q and first scores
+          if (wait1(&fb.q_full, q_tiles++ & 1)) tc_fence_after(), scores();
+        };
+        int cur = tile_steps(0);
+        if (cur > 0) open_tile();
+        for (int w = 0; ok && cur >= 0; ++w) {
+          // the last tile's O must have been read out before the first product overwrites it
+          bool fresh = true;
+          for (int i = 0; i + 1 < cur && ok; ++i) {
+            scores();
+            if (i + 2 == cur && ok) umma2_commit(&fb.q_empty);
+            if (fresh && ok && w > 0) wait1(&fb.o_free, (w - 1) & 1);
+            if (ok) product(step - 2, fresh);
+            fresh = false;
+          }
+          if (!ok) break;
+          if (cur == 1) umma2_commit(&fb.q_empty);
+          const int next = tile_steps(w + 1);
+          if (ok && next > 0) open_tile();
+          if (!ok) break;
+          if (fresh && w > 0 && !wait1(&fb.o_free, (w - 1) & 1)) break;
+          if (cur > 0) product(step - (next > 0 ? 2 : 1), fresh);
+          if (ok) umma2_commit(&fb.o_full);
+          cur = next;
         }
-        if (ok) umma_commit(&fb.pv_done);
+        // every MMA this thread issued has completed once `drain` fires
+        umma2_commit(&fb.drain);
+        mbar_drain_wait(&fb.drain, 0);
       }
-      // every MMA this thread issued has completed once `drain` fires
-      umma_commit(&fb.drain);
-      mbar_drain_wait(&fb.drain, 0);
+      __syncwarp();
     }
-    __syncwarp();
   } else {
-    // ---------------- softmax: thread = row = TMEM lane
-    const int r = warp * 32 + lane;
-    const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
-    const int seen = tile.seen0 + r;  // keys this row sees
-    float m_run = kFaNoMax, l_run = 0.f;
+    regs_grow<kFaRegsSoftmax>();
+    // ---------------- softmax: thread = row = TMEM lane; warpgroup g takes the steps of parity g
+    const int g = warp >> 2, quad = warp & 3;
+    const int r = quad * 32 + lane;
+    const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
+    const uint32_t ts = tmem + lanes + g * kFaN;
+    const uint32_t p_ready = leader_addr(&fb.p_ready[g]), o_free = leader_addr(&fb.o_free);
+    // The reference maximum of a step goes to the warp of the other group with the same rows,
+    // which takes every one of them, in order.
+    auto pass = [&](float m) {
+      fb.m_ref[r] = m;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&fb.m_full[g][quad]);
+    };
+    int taken = 0;
+    auto receive = [&](bool& good) {
+      good = good && wait(&fb.m_full[g ^ 1][quad], taken++ & 1);
+      return fb.m_ref[r];
+    };
+    int step = 0;  // over all query tiles
     bool ok = true;
-    for (int i = 0; i < ntiles; ++i) {
-      const uint32_t ts = tmem + lanes + (i & 1) * kFaN;
-      if (!(ok = mbar_wait_warp(&fb.s_full[i & 1], (i >> 1) & 1, &fb.abort, a.status))) break;
-      tc_fence_after();
-      uint32_t s[128];
+    for (int w = 0; ok; ++w) {
+      if (!(ok = wait(&fb.tile_full[w & 1], (w >> 1) & 1))) break;
+      const FaTile tile = fb.tile[w & 1];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&fb.tile_empty[w & 1]);
+      if (!tile.live) break;
+      const int seen = tile.seen0 + r;  // keys this row sees
+      const int ntiles = (tile.keys + kFaN - 1) / kFaN;
+      float m_run = kFaNoMax, l_run = 0.f;
+      for (int i = 0; i < ntiles; ++i, ++step) {
+        if ((step & 1) != g) continue;
+        ok = ok && wait(&fb.s_full[g], (step >> 1) & 1);
+        tc_fence_after();
+        uint32_t s[128];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_ld32(ts + 32 * c, s + 32 * c);
-      tmem_ld_wait();
-      const int left = seen - i * kFaN;  // columns below this are seen
-      if (__any_sync(0xffffffffu, left < kFaN)) {
+        for (int c = 0; c < 4; ++c) tmem_ld32(ts + 32 * c, s + 32 * c);
+        tmem_ld_wait();
+        const int left = seen - i * kFaN;  // columns below this are seen
+        if (__any_sync(0xffffffffu, left < kFaN)) {
 #pragma unroll
-        for (int c = 0; c < 128; ++c)
-          if (c >= left) s[c] = 0xff800000u;
-      }
-      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          for (int c = 0; c < 128; ++c)
+            if (c >= left) s[c] = 0xff800000u;
+        }
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-      for (int c = 0; c < 128; c += 4)
+        for (int c = 0; c < 128; c += 8)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], __uint_as_float(s[c + e]));
-      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
-      if (__any_sync(0xffffffffu, top > m_run + kFaShift)) {
+          for (int e = 0; e < 4; ++e)
+            mx[e] = fmaxf(mx[e], fmaxf(__uint_as_float(s[c + e]), __uint_as_float(s[c + e + 4])));
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
+        if (i > 0) {  // the reference as the step before left it
+          const float m = receive(ok);
+          l_run *= exp2f(m_run - m);
+          m_run = m;
+        }
         // a row's own decision: its result does not depend on the other rows of the tile
         const float mnew = top > m_run + kFaShift ? top : m_run;
-        const float alpha = exp2f(m_run - mnew);
-        m_run = mnew;
-        l_run *= alpha;
-        if (i > 0) {  // O of this warp's rows, once P_{i-1} V_{i-1} is in
-          if (!(ok = mbar_wait_warp(&fb.pv_done, (i - 1) & 1, &fb.abort, a.status))) break;
-          tc_fence_after();
-          for (int c = 0; c < kD; c += 32) {
-            uint32_t o[32];
-            tmem_ld32(tmem_o + lanes + c, o);
-            tmem_ld_wait();
+        pass(mnew);
+        if (__any_sync(0xffffffffu, mnew != m_run)) {
+          const float alpha = exp2f(m_run - mnew);
+          m_run = mnew;
+          l_run *= alpha;
+          if (i > 0) {  // O of this warp's rows, once the product of the step before is in
+            ok = ok && wait(&fb.pv_done, (step - 1) & 1);
+            tc_fence_after();
+            for (int c = 0; c < kD; c += 32) {
+              uint32_t o[32];
+              tmem_ld32(tmem_o + lanes + c, o);
+              tmem_ld_wait();
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-            tmem_st32(tmem_o + lanes + c, o);
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+              tmem_st32(tmem_o + lanes + c, o);
+            }
+            tmem_st_wait();
           }
-          tmem_st_wait();
+        }
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < 128; c += 4) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float p;
+            asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(p) : "f"(fmaf(__uint_as_float(s[c + e]), a.scale_log2, -m_run)));
+            sum[e] += p;
+            s[c + e] = __float_as_uint(p);
+          }
+          // the pair (c, c + 1) goes into word c / 2
+          if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+            s[c / 2] = pack_bf162(__uint_as_float(s[c]), __uint_as_float(s[c + 1]));
+            s[c / 2 + 1] = pack_bf162(__uint_as_float(s[c + 2]), __uint_as_float(s[c + 3]));
+          } else {
+            s[c / 2] = pack_half2(__uint_as_float(s[c]), __uint_as_float(s[c + 1]));
+            s[c / 2 + 1] = pack_half2(__uint_as_float(s[c + 2]), __uint_as_float(s[c + 3]));
+          }
+        }
+        l_run += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        tmem_st32(ts, s);
+        tmem_st32(ts + 32, s + 32);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_at(p_ready);
+      }
+      // ---------------- both groups' sums, relative to the last reference
+      if (ntiles > 0 && ((step - 1) & 1) != g) {
+        const float m = receive(ok);
+        l_run *= exp2f(m_run - m);
+      }
+      if (w > 0) ok = ok && wait(&fb.l_free[quad], (w - 1) & 1);
+      fb.l_part[g][r] = l_run;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&fb.l_full[quad]);
+      ok = ok && wait(&fb.l_full[quad], w & 1);
+      const float l = fb.l_part[0][r] + fb.l_part[1][r];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&fb.l_free[quad]);
+      const float inv = l > 0.f ? 1.f / l : 0.f;
+      // ---------------- this group's half of O / l, gated
+      const bool mine = r < tile.rows;
+      const int64_t row = tile.row0 + r;
+      const int d0 = tile.head * kD + 128 * g;
+      uint4 x[16];  // the row's gate, then its output, as 16-bit values
+      if (a.gate && mine) {
+        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T*>(a.gate) + row * a.ldg + d0);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) x[j] = __ldg(src + j);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) x[j] = make_uint4(0u, 0u, 0u, 0u);
+      }
+      ok = ok && wait(&fb.o_full, w & 1);
+      tc_fence_after();
+      // O leaves TMEM before anything is stored: the next tile's first product waits for it
+#pragma unroll
+      for (int c = 0; c < 128; c += 32) {
+        uint32_t o[32];
+        tmem_ld32(tmem_o + lanes + 128 * g + c, o);
+        tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float y[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) y[e] = l > 0.f ? __uint_as_float(o[8 * j + e]) * inv : 0.f;
+          if (a.gate) {
+            Row8<T> graw;
+            graw.a = x[c / 8 + j];
+            float gv[8];
+            graw.get(gv);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] *= gate_factor(gv[e]);
+          }
+          x[c / 8 + j] = Row8<T>::pack(y);
         }
       }
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int c = 0; c < 128; c += 4) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float p;
-          asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(p) : "f"(fmaf(__uint_as_float(s[c + e]), a.scale_log2, -m_run)));
-          sum[e] += p;
-          s[c + e] = __float_as_uint(p);
-        }
-        // the pair (c, c + 1) goes into word c / 2
-        if constexpr (std::is_same<T, __nv_bfloat16>::value) {
-          s[c / 2] = pack_bf162(__uint_as_float(s[c]), __uint_as_float(s[c + 1]));
-          s[c / 2 + 1] = pack_bf162(__uint_as_float(s[c + 2]), __uint_as_float(s[c + 3]));
-        } else {
-          s[c / 2] = pack_half2(__uint_as_float(s[c]), __uint_as_float(s[c + 1]));
-          s[c / 2 + 1] = pack_half2(__uint_as_float(s[c + 2]), __uint_as_float(s[c + 3]));
-        }
-      }
-      l_run += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-      tmem_st32(ts, s);
-      tmem_st32(ts + 32, s + 32);
-      tmem_st_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&fb.p_ready[i & 1]);
-    }
-    // ---------------- O / l, gated
-    if (ok && ntiles > 0) ok = mbar_wait_warp(&fb.pv_done, (ntiles - 1) & 1, &fb.abort, a.status);
-    if (ok) {
-      tc_fence_after();
-      const float inv = l_run > 0.f ? 1.f / l_run : 0.f;
-      const bool mine = r < tile.rows;
-      const int row = tile.row0 + r;
-      T* dst = static_cast<T*>(a.out) + row * a.ldo + head * kD;
-      const T* gsrc = a.gate ? static_cast<const T*>(a.gate) + row * a.ldg + head * kD : nullptr;
-      for (int c = 0; c < kD; c += 32) {
-        uint32_t o[32];
-        if (ntiles > 0) {
-          tmem_ld32(tmem_o + lanes + c, o);
-          tmem_ld_wait();
-        }
-        if (mine) {
+      if (lane == 0) mbar_arrive_at(o_free);
+      if (mine && ok) {
+        uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(a.out) + row * a.ldo + d0);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            float x[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = l_run > 0.f ? __uint_as_float(o[8 * j + e]) * inv : 0.f;
-            if (gsrc) {
-              Row8<T> graw;
-              graw.load(gsrc + c + 8 * j);
-              float gv[8];
-              graw.get(gv);
-#pragma unroll
-              for (int e = 0; e < 8; ++e) x[e] *= gate_factor(gv[e]);
-            }
-            Row8<T>::store(dst + c + 8 * j, x);
-          }
-        }
-        __syncwarp();
+        for (int j = 0; j < 16; ++j) dst[j] = x[j];
       }
     }
   }
   tc_fence_before();
   __syncthreads();
+  cluster_sync_all();  // nothing of the pair reads or signals the other CTA any more
   tc_fence_after();
-  if (warp == 5) tmem_dealloc(tmem, 512u);
+  if (warp == 9) tmem2_dealloc(tmem, 512u);
 }
 
 }  // namespace qsa
