@@ -362,6 +362,9 @@ int qsa_paged_decode(const qsa_paged_cache* cache, const qsa_batch* batch, int r
                      int64_t ldg, float scale, void* ws, size_t ws_bytes, void* out, int64_t ldo,
                      void* stream);
 
+/* Workspace bytes of qsa_prompt_attn: 0 where it needs none (and for sizes that it refuses). */
+size_t qsa_prompt_attn_workspace_bytes(int nseq, int rows_q, int rows_k, int hq, int hkv);
+
 /*
  * Causal attention over whole prompts, packed one after the other: sequence s has the query
  * rows cu_q[s] .. cu_q[s+1] - 1 and the key rows cu_k[s] .. cu_k[s+1] - 1 ([nseq + 1] each,
@@ -371,13 +374,15 @@ int qsa_paged_decode(const qsa_paged_cache* cache, const qsa_batch* batch, int r
  * and is 0 when it sees none.  q, gate (or NULL), out [rows_q][hq][256] and k, v
  * [rows_k][hkv][256] of QSA_F16 or QSA_BF16 (the tensor cores' types: fp32 rows are refused,
  * fp32 callers cast or use the paged cache).  Rows at or past cu_q[nseq] are left as they were;
- * what lies behind a sequence's keys is not used, whatever it holds.  Waits are bounded and
- * report through qsa_device_status.
+ * what lies behind a sequence's keys is not used, whatever it holds.  Few rows against many
+ * keys are split over the keys and joined through ws (qsa_prompt_attn_workspace_bytes(...) bytes,
+ * one call at a time; may be NULL where that is 0).  The result is the same in every run.  Waits
+ * are bounded and report through qsa_device_status.
  */
 int qsa_prompt_attn(int nseq, const int32_t* cu_q, const int32_t* cu_k, int rows_q, int rows_k,
                     int dtype, int hq, int hkv, const void* q, int64_t ldq, const void* k,
                     int64_t ldk, const void* v, int64_t ldv, const void* gate, int64_t ldg,
-                    float scale, void* out, int64_t ldo, void* stream);
+                    float scale, void* ws, size_t ws_bytes, void* out, int64_t ldo, void* stream);
 
 /*
  * Device-side failure report.  Kernels that wait on an mbarrier (the prefill

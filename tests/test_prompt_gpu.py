@@ -109,6 +109,16 @@ def test_prompt_head_layouts(gpu, hq, hkv):
     check(gpu, [140, 33], [140, 50], hq, hkv, torch.float16)
 
 
+@pytest.mark.parametrize("n,m,hq,hkv", [([3], [9000], 24, 2), ([1, 130], [3000, 5000], 6, 2), ([140], [6000], 3, 1),
+                                        ([300, 0, 2], [4000, 0, 1], 5, 5), ([2, 2], [1, 8000], 4, 2)])
+def test_prompt_keys_in_parts(gpu, n, m, hq, hkv):
+    """Few rows against many keys: the keys are cut and joined, also for sequences whose keys fill
+    one part only, or none."""
+    assert gpu.prompt_attn_workspace_bytes(len(n), sum(n) + 5, sum(m) + 5, hq, hkv) > 0
+    check(gpu, n, m, hq, hkv, torch.float16, gated=True)
+    check(gpu, n, m, hq, hkv, torch.bfloat16)
+
+
 @pytest.mark.parametrize("dtype", TYPES)
 def test_prompt_large_scores(gpu, dtype):
     """Scores of tens and rising maxima: O is rescaled along the keys."""

@@ -3,6 +3,7 @@
 // launches; the computation is in the kernels of the qsa_paged_*.cuh and qsa_prompt_attn.cuh files.
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <type_traits>
 
 #include "qsa_host.h"
@@ -181,10 +182,61 @@ int encode_rows(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap* map, cons
   return QSA_OK;
 }
 
-template <typename T>
+// ---- prompt plan
+
+struct PromptPlan {
+  int by_heads, parts;
+  int64_t pairs;  // of the grid, parts included
+  size_t part_o, part_ml, total;
+};
+
+// A pair of CTAs takes two heads of a KV head where their number is even: both then see the same
+// keys, while two row blocks of one head differ by a tile.  Every block of a sequence but its last
+// is full, which bounds the pairs.  Their keys are cut into parts where that makes the call
+// shorter by this estimate in key tiles (1.5 us each on the device): rounds of `pairs_at_once`
+// pairs, a tile's fixed cost of about four key tiles, and a part's rows written and read again
+// (two thirds of a microsecond for a hundred pairs) with one more launch.  16 rows of 24 heads at
+// 32768 keys: 12 pairs of 256 key tiles, 437 us whole and 70 us in 12 parts.
+PromptPlan plan_prompt(int nseq, int rows_q, int rows_k, int hq, int hkv) {
+  PromptPlan p;
+  constexpr int pairs_at_once = 74;
+  p.by_heads = (hq / hkv) % 2 == 0;
+  const int block_rows = p.by_heads ? qsa::kFaM : 2 * qsa::kFaM, sets = p.by_heads ? hq / 2 : hq;
+  const int most = std::min(nseq, rows_q);  // sequences with rows
+  const int64_t whole = (static_cast<int64_t>(rows_q - most) / block_rows + most) * sets;
+  const double tiles = std::max(1.0, static_cast<double>(rows_k) / nseq / qsa::kFaN);
+  double best = 0;
+  p.parts = 1;
+  for (int n = 1; n <= 32 && n <= tiles / 4 + 1; ++n) {
+    const double rounds = static_cast<double>((whole * n + pairs_at_once - 1) / pairs_at_once);
+    const double cost = rounds * (std::ceil(tiles / n) + 4) + (n > 1 ? 3 + 0.05 * whole * n : 0.0);
+    if (n == 1 || cost < 0.95 * best) {
+      best = cost;
+      p.parts = n;
+    }
+  }
+  p.pairs = whole * p.parts;
+  p.part_o = 0;
+  p.part_ml = p.parts > 1 ? align_up(static_cast<size_t>(p.pairs) * 2 * qsa::kFaM * QSA_D * 4, 256) : 0;
+  p.total = p.parts > 1 ? align_up(p.part_ml + static_cast<size_t>(p.pairs) * 2 * qsa::kFaM * 8, 256) : 0;
+  return p;
+}
+
+int check_prompt_sizes(int nseq, int rows_q, int rows_k, int hq, int hkv) {
+  if (hkv < 1 || hkv > QSA_MAX_HEADS || hq < 1 || hq > QSA_MAX_HEADS || hq % hkv)
+    return fail(QSA_ERR_ARG, "hq = %d must be a multiple of hkv = %d, both in [1, %d]", hq, hkv, QSA_MAX_HEADS);
+  if (nseq < 1 || nseq > QSA_MAX_ROWS) return fail(QSA_ERR_ARG, "nseq = %d out of [1, %d]", nseq, QSA_MAX_ROWS);
+  if (rows_q < 0 || rows_q > QSA_MAX_PACKED || rows_k < 0 || rows_k > QSA_MAX_PACKED)
+    return fail(QSA_ERR_ARG, "rows_q = %d, rows_k = %d out of [0, %d]", rows_q, rows_k, QSA_MAX_PACKED);
+  if (plan_prompt(nseq, rows_q, rows_k, hq, hkv).pairs >= (static_cast<int64_t>(1) << 30))
+    return fail(QSA_ERR_ARG, "rows_q = %d x hq = %d out of range", rows_q, hq);
+  return QSA_OK;
+}
+
+template <typename T, bool kGate>
 cudaError_t launch_prompt(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const qsa::FaArgs& a,
                           int pairs, cudaStream_t s) {
-  auto kernel = qsa::prompt_attn_kernel<T>;
+  auto kernel = qsa::prompt_attn_kernel<T, kGate>;
   static std::atomic<uint64_t> done{0};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -196,6 +248,18 @@ cudaError_t launch_prompt(const CUtensorMap& q, const CUtensorMap& k, const CUte
     done.fetch_or(bit, std::memory_order_relaxed);
   }
   return launch_pdl(kernel, dim3(2 * pairs), dim3(qsa::kFaThreads), qsa::kFaSmemBytes, s, q, k, v, a);
+}
+
+template <typename T>
+int launch_prompt_step(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const qsa::FaArgs& a,
+                       int pairs, cudaStream_t s) {
+  // the gate is the join's where there is one
+  const cudaError_t e = a.gate && a.parts == 1 ? launch_prompt<T, true>(q, k, v, a, pairs, s)
+                                               : launch_prompt<T, false>(q, k, v, a, pairs, s);
+  const int r = launched("prompt_attn_kernel", e);
+  if (r || a.parts == 1) return r;
+  return launched("prompt_join_kernel", launch_pdl(qsa::prompt_join_kernel<T>, dim3(a.rows_q, (a.hq + 7) / 8), dim3(256),
+                                                   0, s, a));
 }
 
 }  // namespace
@@ -287,17 +351,19 @@ int qsa_paged_decode(const qsa_paged_cache* cache, const qsa_batch* batch, int r
   return ok();
 }
 
+size_t qsa_prompt_attn_workspace_bytes(int nseq, int rows_q, int rows_k, int hq, int hkv) {
+  if (check_prompt_sizes(nseq, rows_q, rows_k, hq, hkv)) return 0;
+  return plan_prompt(nseq, rows_q, rows_k, hq, hkv).total;
+}
+
 int qsa_prompt_attn(int nseq, const int32_t* cu_q, const int32_t* cu_k, int rows_q, int rows_k, int dtype, int hq,
                     int hkv, const void* q, int64_t ldq, const void* k, int64_t ldk, const void* v, int64_t ldv,
-                    const void* gate, int64_t ldg, float scale, void* out, int64_t ldo, void* stream) {
+                    const void* gate, int64_t ldg, float scale, void* ws, size_t ws_bytes, void* out, int64_t ldo,
+                    void* stream) {
   int r;
   if (dtype != QSA_F16 && dtype != QSA_BF16)
     return fail(QSA_ERR_ARG, "dtype = %d: prompt attention takes QSA_F16 or QSA_BF16 rows", dtype);
-  if (hkv < 1 || hkv > QSA_MAX_HEADS || hq < 1 || hq > QSA_MAX_HEADS || hq % hkv)
-    return fail(QSA_ERR_ARG, "hq = %d must be a multiple of hkv = %d, both in [1, %d]", hq, hkv, QSA_MAX_HEADS);
-  if (nseq < 1 || nseq > QSA_MAX_ROWS) return fail(QSA_ERR_ARG, "nseq = %d out of [1, %d]", nseq, QSA_MAX_ROWS);
-  if (rows_q < 0 || rows_q > QSA_MAX_PACKED || rows_k < 0 || rows_k > QSA_MAX_PACKED)
-    return fail(QSA_ERR_ARG, "rows_q = %d, rows_k = %d out of [0, %d]", rows_q, rows_k, QSA_MAX_PACKED);
+  if ((r = check_prompt_sizes(nseq, rows_q, rows_k, hq, hkv))) return r;
   if (!cu_q || !cu_k) return fail(QSA_ERR_ARG, "cu_q and cu_k must not be NULL");
   if (rows_q == 0) return ok();
   if ((r = check_rows("q", q, ldq, hq, dtype)) || (r = check_rows("out", out, ldo, hq, dtype)) ||
@@ -309,6 +375,10 @@ int qsa_prompt_attn(int nseq, const int32_t* cu_q, const int32_t* cu_k, int rows
   } else if ((r = check_rows("k", k, ldk, hkv, dtype)) || (r = check_rows("v", v, ldv, hkv, dtype))) {
     return r;
   }
+  const PromptPlan p = plan_prompt(nseq, rows_q, rows_k, hq, hkv);
+  if (ws_bytes < p.total || (p.total && !ws))
+    return fail(QSA_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", ws ? ws_bytes : static_cast<size_t>(0), p.total);
+  if (p.total && !aligned16(ws)) return fail(QSA_ERR_ARG, "ws must be 16-byte aligned");
   if ((r = prepare_device())) return r;
   PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
   if ((r = tensor_map_encoder(&encode))) return r;
@@ -325,23 +395,20 @@ int qsa_prompt_attn(int nseq, const int32_t* cu_q, const int32_t* cu_k, int rows
   a.rows_k = rows_k;
   a.hq = hq;
   a.group = hq / hkv;
+  a.by_heads = p.by_heads;
+  a.parts = p.parts;
+  a.part_o = reinterpret_cast<float*>(static_cast<char*>(ws) + p.part_o);
+  a.part_ml = reinterpret_cast<float2*>(static_cast<char*>(ws) + p.part_ml);
   a.scale_log2 = scale * 1.4426950408889634f;
   a.gate = gate;
   a.out = out;
   a.ldg = ldg;
   a.ldo = ldo;
   a.status = device_status();
-  // A pair of CTAs takes two heads of a KV head where their number is even: both then see the
-  // same keys, while two row blocks of one head differ by a tile.
-  a.by_heads = a.group % 2 == 0;
-  const int block_rows = a.by_heads ? qsa::kFaM : 2 * qsa::kFaM, sets = a.by_heads ? hq / 2 : hq;
-  // every block of a sequence but its last is full, so there are at most this many
-  const int64_t pairs = (static_cast<int64_t>(rows_q) / block_rows + std::min(nseq, rows_q)) * sets;
-  if (pairs >= (static_cast<int64_t>(1) << 30)) return fail(QSA_ERR_ARG, "rows_q = %d x hq = %d out of range", rows_q, hq);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = dtype == QSA_F16 ? launch_prompt<__half>(tq, tk, tv, a, static_cast<int>(pairs), s)
-                                         : launch_prompt<__nv_bfloat16>(tq, tk, tv, a, static_cast<int>(pairs), s);
-  if ((r = launched("prompt_attn_kernel", e))) return r;
+  r = dtype == QSA_F16 ? launch_prompt_step<__half>(tq, tk, tv, a, static_cast<int>(p.pairs), s)
+                       : launch_prompt_step<__nv_bfloat16>(tq, tk, tv, a, static_cast<int>(p.pairs), s);
+  if (r) return r;
   return ok();
 }
 

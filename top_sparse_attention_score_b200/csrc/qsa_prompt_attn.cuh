@@ -10,7 +10,7 @@
 // tensor cores need: a single CTA's product of 128 rows reads as much shared memory as the
 // tensor cores take time (8 KB per 64 cycles, with the loads' writes on top), and every SM would
 // fetch all of K and V; a pair halves both.  Per CTA:
-//   * Q (128 x 256) stays in shared memory; tiles of 128 keys stream through a ring of five
+//   * Q (128 x 256) stays in shared memory; tiles of 128 keys stream through a ring of four
 //     32 KB slots that one thread fills by TMA: of K its 64 keys, of V its 128 dims;
 //   * the leader CTA's MMA thread issues S_i = Q K_i^T into one of two 128-column TMEM buffers,
 //     then O += P_i V_i with P_i read from TMEM (the weights overwrite their scores as 16-bit
@@ -18,8 +18,11 @@
 //   * two softmax warpgroups take the key tiles in turn, a thread a row, so one exchanges nothing
 //     but the row's reference maximum with the other, and the exponentials of one overlap the
 //     TMEM traffic of the other.  The reference moves only when a tile exceeds it by more than
-//     2^8, so O is rarely rescaled.  At a tile's end each reads half of O out (divide, gate,
-//     store) while the next tile's scores are computed;
+//     2^8, so O is rarely rescaled.  At a tile's end one reads O out (divide, gate, store) while
+//     the other begins with the next tile; rows go through shared memory to be stored whole
+//     (a thread storing its own row in pieces of 16 bytes took 4 us a tile);
+//   * where the query tiles are few for the GPU and the keys many, a tile's keys are cut into
+//     parts that pairs compute on their own, joined by a second kernel;
 //   * the grid has a pair per query tile; a running pair takes over one that has not started
 //     through cluster launch control, so the next tile's loads overlap the end of this one.
 //
@@ -29,6 +32,7 @@
 // Every mbarrier wait is bounded and reports through the device status word.
 #pragma once
 
+#include "qsa_attn.cuh"
 #include "qsa_paged_cache.cuh"
 #include "qsa_sm100.cuh"
 
@@ -36,9 +40,10 @@ namespace qsa {
 
 constexpr int kFaM = 128;      // query rows of a CTA
 constexpr int kFaN = 128;      // keys of a tile
-constexpr int kFaSlots = 5;
+constexpr int kFaSlots = 4;
 constexpr int kFaSlotBytes = 32 * 1024;  // a CTA's half of a K or V tile
 constexpr int kFaQBytes = kFaM * kD * 2;
+constexpr int kFaOutBytes = 4 * 32 * 64 * 4;  // staging of four warps' 32 rows, 64 fp32 dims at a time
 // Three warpgroups: two of softmax; TMA, MMA and two idle warps.  The softmax holds a row's 128
 // scores in registers, so it takes some from the others.
 constexpr int kFaThreads = 384;
@@ -54,9 +59,10 @@ constexpr float kFaNoMax = -1.0e30f;
 struct FaTile {
   int live;        // 0: no more tiles
   int row0, rows;  // this CTA's first packed query row; its rows (<= 0: none)
-  int key0, keys;  // first packed key row; keys that any row of the pair sees
-  int seen0;       // keys that this CTA's first row sees (row r sees seen0 + r)
+  int key0, keys;  // first packed key row; keys of this part that any row of the pair sees
+  int seen0;       // keys of it that this CTA's first row sees (row r sees seen0 + r)
   int head;
+  int pair;        // index of the pair in the grid
 };
 
 // (L): only the leader CTA's is used, by both CTAs.
@@ -72,18 +78,19 @@ struct __align__(16) FaBarriers {
   uint64_t p_ready[2];           // (L) four warps of each CTA
   uint64_t pv_done;              // one phase per key tile
   uint64_t o_full;               // one phase per query tile: O complete
-  uint64_t o_free;               // (L) read out: eight warps of each CTA
+  uint64_t o_free;               // (L) read out: four warps of each CTA
   uint64_t tile_full[2], tile_empty[2];
   uint64_t tail, drain;
   FaTile tile[2];
   uint64_t m_full[2][4];         // a group's warp has passed its rows' reference maxima
-  uint64_t l_full[4], l_free[4]; // both groups' sums of a warp's rows are there; were read
+  uint64_t l_full[4], l_free[4]; // one group's sums of a warp's rows are there; were read
   float m_ref[kFaM];             // the rows' reference maxima, passed between the warpgroups
-  float l_part[2][kFaM];
+  float l_part[kFaM];            // the rows' sums of the group that does not read O out
   uint32_t tmem_base;
   uint32_t abort;
 };
-constexpr int kFaSmemBytes = 1024 /*align*/ + kFaQBytes + kFaSlots * kFaSlotBytes + static_cast<int>(sizeof(FaBarriers));
+constexpr int kFaSmemBytes = 1024 /*align*/ + kFaQBytes + kFaSlots * kFaSlotBytes + kFaOutBytes +
+                             static_cast<int>(sizeof(FaBarriers));
 static_assert(kFaSmemBytes <= 227 * 1024, "shared memory of a CTA");
 
 struct FaArgs {
@@ -93,6 +100,9 @@ struct FaArgs {
   int rows_q, rows_k;
   int hq, group;
   int by_heads;  // a pair is two heads (else two blocks of rows)
+  int parts;     // pieces of a tile's keys, each a tile of its own, joined afterwards
+  float* part_o;    // parts > 1: [pairs of the grid][2][128][256] unnormalised rows
+  float2* part_ml;  // [pairs of the grid][2][128]: reference (log2 units), sum
   float scale_log2;
   const void* gate;
   void* out;
@@ -123,7 +133,38 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
       "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n" ::"r"(
+          taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
+
+// Two fp32 values in a 64-bit register, for the two-wide instructions.
+__device__ __forceinline__ uint64_t pack_u32x2(uint32_t a, uint32_t b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t pack_f32x2(float a, float b) {
+  return pack_u32x2(__float_as_uint(a), __float_as_uint(b));
+}
+__device__ __forceinline__ void unpack_f32x2(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 
 template <int N>
 __device__ __forceinline__ void regs_grow() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N)); }
@@ -166,6 +207,13 @@ __device__ __forceinline__ void tma_load_3d_pair(void* dst, const CUtensorMap* m
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar_cluster_addr)
       : "memory");
 }
+// Into L2 only.
+__device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap* map, int x, int y, int z) {
+  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global [%0, {%1, %2, %3}];\n" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(x), "r"(y), "r"(z)
+               : "memory");
+}
 __device__ __forceinline__ void umma2_f16_ss(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                              uint32_t accumulate) {
   asm volatile(
@@ -199,11 +247,18 @@ __device__ __forceinline__ void tmem2_dealloc(uint32_t base, uint32_t cols) {
   asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;\n" ::"r"(base), "r"(cols));
 }
 
-// Bounded wait by try_wait: the thread sleeps in hardware until the phase completes or a short
-// limit of the hardware's passes, so waiting takes few issue slots from the warps that work; the
-// clock (a read of %globaltimer is slow) and the abort flag are read only when it returns
-// without the phase.
+// Whether the phase has completed, without waiting.
+__device__ __forceinline__ bool fa_test(uint64_t* bar, uint32_t parity) {
+  return mbar_try<false>(smem_u32(bar), parity);
+}
+
+// Bounded wait: one test, then try_wait, in which the thread sleeps in hardware until the phase
+// completes or a short limit of the hardware's passes.  Polling instead takes issue slots from
+// the warps that work (740 us where this takes 620, at 8192 causal rows of 24 heads), and try_wait
+// alone is slower to see a phase that has long completed (660 us).  The clock (a read of
+// %globaltimer is slow) and the abort flag are read only when it returns without the phase.
 __device__ __forceinline__ bool fa_wait(uint64_t* bar, uint32_t parity, uint32_t* abort, uint32_t* status) {
+  if (fa_test(bar, parity)) return true;
   const uint32_t addr = smem_u32(bar);
   unsigned long long t0 = 0ull;
   for (;;) {
@@ -268,14 +323,14 @@ __device__ __forceinline__ int fa_blocks(const FaArgs& a, int s, int block_rows)
   return (max(0, n) + block_rows - 1) / block_rows;
 }
 
-// The part of CTA `rank` of pair `pair` of the grid: heads fastest (they share K and V through
-// L2), then row blocks, the last first (a sequence's last block sees the most keys, so the
-// longest work starts first).  The warp computes it together.
+// The work of CTA `rank` of pair `pair` of the grid: heads fastest (they share K and V through
+// L2), then parts of the keys, then row blocks, the last first (a sequence's last block sees the
+// most keys, so the longest work starts first).  The warp computes it together.
 __device__ __forceinline__ FaTile fa_tile(const FaArgs& a, int pair, int rank) {
   const int lane = threadIdx.x & 31;
   const int sets = a.by_heads ? a.hq / 2 : a.hq, block_rows = a.by_heads ? kFaM : 2 * kFaM;
-  const int idx = pair / sets;
-  FaTile t = {0, 0, 0, 0, 0, 0, 0};
+  const int part = (pair / sets) % a.parts, idx = pair / sets / a.parts;
+  FaTile t = {0, 0, 0, 0, 0, 0, 0, pair};
   t.head = a.by_heads ? 2 * (pair % sets) + rank : pair % sets;
   int total = 0;
   for (int s0 = 0; s0 < a.nseq; s0 += 32) total += fa_blocks(a, s0 + lane, block_rows);
@@ -301,9 +356,12 @@ __device__ __forceinline__ FaTile fa_tile(const FaArgs& a, int pair, int rank) {
       t.live = 1;
       t.row0 = q0 + first + off;
       t.rows = min(kFaM, n - first - off);
-      t.key0 = k0;
-      t.seen0 = first + off + 1 + m - n;
-      t.keys = max(0, min(m, m - n + min(n, first + block_rows)));
+      const int keys = max(0, min(m, m - n + min(n, first + block_rows)));
+      const int tiles = (keys + kFaN - 1) / kFaN;
+      const int from = min(keys, (tiles + a.parts - 1) / a.parts * part * kFaN);
+      t.key0 = k0 + from;
+      t.keys = min(keys - from, (tiles + a.parts - 1) / a.parts * kFaN);
+      t.seen0 = first + off + 1 + m - n - from;
       return t;
     }
     base += __shfl_sync(0xffffffffu, inc, 31);
@@ -311,9 +369,13 @@ __device__ __forceinline__ FaTile fa_tile(const FaArgs& a, int pair, int rank) {
   return t;
 }
 
+// sigmoid(g) by the hardware's 2^x and reciprocal (2^-21 relative; the result is rounded to 16
+// bits at once, and the exact division's code would fill the instruction cache).
+__device__ __forceinline__ float fa_gate(float g) { return __fdividef(1.f, 1.f + attn_exp2(g * -1.4426950408889634f)); }
+
 // grid: 2 * pairs (head sets * an upper bound of the row blocks), clusters of 2; block: 384;
 // dynamic shared memory: kFaSmemBytes.
-template <typename T>
+template <typename T, bool kGate>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFaThreads, 1)
     prompt_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
                        const __grid_constant__ CUtensorMap tmap_v, FaArgs a) {
@@ -325,7 +387,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFaThreads, 1)
       reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(fsm_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   unsigned char* sq = fsm;
   unsigned char* ring = fsm + kFaQBytes;
-  FaBarriers& fb = *reinterpret_cast<FaBarriers*>(ring + kFaSlots * kFaSlotBytes);
+  unsigned char* stage = ring + kFaSlots * kFaSlotBytes;
+  FaBarriers& fb = *reinterpret_cast<FaBarriers*>(stage + kFaOutBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = static_cast<int>(cluster_rank());
   auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -354,12 +417,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFaThreads, 1)
     for (int i = 0; i < 4; ++i) {
       mbar_init(&fb.m_full[0][i], 1);
       mbar_init(&fb.m_full[1][i], 1);
-      mbar_init(&fb.l_full[i], 2);
-      mbar_init(&fb.l_free[i], 2);
+      mbar_init(&fb.l_full[i], 1);
+      mbar_init(&fb.l_free[i], 1);
     }
     mbar_init(&fb.pv_done, 1);
     mbar_init(&fb.o_full, 1);
-    mbar_init(&fb.o_free, 16);
+    mbar_init(&fb.o_free, 8);
     mbar_init(&fb.tail, 1);
     mbar_init(&fb.drain, 1);
     fb.abort = 0u;
@@ -447,8 +510,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFaThreads, 1)
           }
         }
         const int ntiles = tile.live ? (tile.keys + kFaN - 1) / kFaN : 0;
-        if (ntiles > 0) {
-          if (!(ok = wait(&fb.q_empty, (loads_q & 1) ^ 1))) break;
+        auto load_q = [&]() {
+          if (!(ok = ok && wait(&fb.q_empty, (loads_q & 1) ^ 1))) return;
           ++loads_q;
           if (lane == 0) {
             const uint32_t bar = leader_addr(&fb.q_full);
@@ -456,9 +519,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFaThreads, 1)
             for (int c = 0; c < 4; ++c)
               tma_load_3d_pair(sq + c * (kFaM * 128), &tmap_q, 64 * c, tile.head, tile.row0, bar);
           }
-          load_k(tile, 0);
-        }
-        if (ok && last.keys > 0) load_v(last, (last.keys - 1) / kFaN);
+        };
+        const bool held = last.keys > 0;  // Q is in use until the last tile's scores are complete
+        if (ntiles > 0 && !held) load_q();
+        if (ntiles > 0 && ok) load_k(tile, 0);
+        if (held && ok) load_v(last, (last.keys - 1) / kFaN);
+        if (ntiles > 0 && held) load_q();
         last.keys = 0;
         if (!ok || !tile.live) break;
         // the next tile is looked up behind K_1: before this tile's last V, which follows the
@@ -475,6 +541,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFaThreads, 1)
             if (rank == 1 && lane == 0) mbar_arrive_at(leader_addr(&fb.next_free));
             next.live = 0;
             if (got >= 0) next = fa_tile(a, got / 2, rank);
+            // its Q comes from HBM and has to wait for this tile's last scores: into L2 now
+            if (next.live && lane < 4) tma_prefetch_3d(&tmap_q, 64 * lane, next.head, next.row0);
+            __syncwarp();
           }
           if (ok && i < ntiles) load_v(tile, i - 1);
         }
@@ -501,17 +570,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFaThreads, 1)
         int q_tiles = 0;
         const uint32_t q0 = smem_u32(sq), r0 = smem_u32(ring);
         auto wait1 = [&](uint64_t* bar, uint32_t parity) { return ok = fa_wait(bar, parity, &fb.abort, a.status); };
-        auto take = [&](int& slot) {
-          slot = n % kFaSlots;
-          wait1(&fb.full[slot], (n / kFaSlots) & 1);
-          ++n;
+        auto take = [&](int at) {  // slot of the at-th K or V tile
+          wait1(&fb.full[at % kFaSlots], (at / kFaSlots) & 1);
           tc_fence_after();
-          return ok;
+          return at % kFaSlots;
         };
-        auto scores = [&]() {  // S = Q K_step^T
-          const int b = step & 1;
-          int slot;
-          if (!take(slot)) return;
+        auto scores = [&](int at) {  // S = Q K_step^T
+          const int b = step & 1, slot = take(at);
+          if (!ok) return;
 #pragma unroll
           for (int ks = 0; ks < 16; ++ks)
             umma2_f16_ss(tmem + b * kFaN, umma_desc_k_sw128(q0 + (ks >> 2) * (kFaM * 128) + (ks & 3) * 32, 1024),
@@ -521,10 +587,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFaThreads, 1)
           umma2_commit(&fb.s_full[b]);
           ++step;
         };
-        auto product = [&](int j, bool fresh) {  // O (+)= P_j V_j
+        auto product = [&](int j, bool fresh, int at) {  // O (+)= P_j V_j
           const int b = j & 1;
-          int slot;
-          if (!wait1(&fb.p_ready[b], (j >> 1) & 1) || !take(slot)) return;
+          if (!wait1(&fb.p_ready[b], (j >> 1) & 1)) return;
+          const int slot = take(at);
+          if (!ok) return;
 #pragma unroll
           for (int ks = 0; ks < 8; ++ks)
             umma2_f16_ts(tmem_o, tmem + b * kFaN + ks * 8,
@@ -539,28 +606,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFaThreads, 1)
           mbar_arrive(&fb.tile_empty[w & 1]);
           return live ? (keys + kFaN - 1) / kFaN : -1;
         };
-        auto open_tile = [&]() {  // its Q and first scores
-          if (wait1(&fb.q_full, q_tiles++ & 1)) tc_fence_after(), scores();
+        auto open_tile = [&](int at) {  // its Q and first scores
+          if (wait1(&fb.q_full, q_tiles++ & 1)) tc_fence_after(), scores(at);
         };
         int cur = tile_steps(0);
-        if (cur > 0) open_tile();
+        if (cur > 0) open_tile(n++);
         for (int w = 0; ok && cur >= 0; ++w) {
           // the last tile's O must have been read out before the first product overwrites it
           bool fresh = true;
+          auto o_free = [&]() {
+            if (fresh && w > 0) wait1(&fb.o_free, (w - 1) & 1);
+            return ok;
+          };
           for (int i = 0; i + 1 < cur && ok; ++i) {
-            scores();
+            scores(n++);
             if (i + 2 == cur && ok) umma2_commit(&fb.q_empty);
-            if (fresh && ok && w > 0) wait1(&fb.o_free, (w - 1) & 1);
-            if (ok) product(step - 2, fresh);
+            if (ok && o_free()) product(step - 2, fresh, n++);
             fresh = false;
           }
           if (!ok) break;
           if (cur == 1) umma2_commit(&fb.q_empty);
           const int next = tile_steps(w + 1);
-          if (ok && next > 0) open_tile();
           if (!ok) break;
-          if (fresh && w > 0 && !wait1(&fb.o_free, (w - 1) & 1)) break;
-          if (cur > 0) product(step - (next > 0 ? 2 : 1), fresh);
+          if (next > 0 && (cur == 0 || fa_test(&fb.q_full, q_tiles & 1))) {
+            // the next tile's Q is there: its first scores go ahead of this tile's last product
+            open_tile(n++);
+            if (ok && o_free() && cur > 0) product(step - 2, fresh, n++);
+          } else {
+            if (o_free() && cur > 0) product(step - 1, fresh, next > 0 ? n + 1 : n);
+            if (ok && next > 0) open_tile(n);
+            n += (cur > 0) + (next > 0);
+          }
           if (ok) umma2_commit(&fb.o_full);
           cur = next;
         }
@@ -637,6 +713,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFaThreads, 1)
           if (i > 0) {  // O of this warp's rows, once the product of the step before is in
             ok = ok && wait(&fb.pv_done, (step - 1) & 1);
             tc_fence_after();
+#pragma unroll 1
             for (int c = 0; c < kD; c += 32) {
               uint32_t o[32];
               tmem_ld32(tmem_o + lanes + c, o);
@@ -648,91 +725,120 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFaThreads, 1)
             tmem_st_wait();
           }
         }
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        // two elements an instruction where there is one (fma, add, conversion)
+        const uint64_t scale2 = pack_f32x2(a.scale_log2, a.scale_log2), m2 = pack_f32x2(-m_run, -m_run);
+        uint64_t sum[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
-        for (int c = 0; c < 128; c += 4) {
+        for (int c = 0; c < 128; c += 32) {
+          uint32_t p[16];  // the pair (c + 2 e, c + 2 e + 1) in word e
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float p;
-            asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(p) : "f"(fmaf(__uint_as_float(s[c + e]), a.scale_log2, -m_run)));
-            sum[e] += p;
-            s[c + e] = __float_as_uint(p);
+          for (int e = 0; e < 16; ++e) {
+            const uint64_t x = fma_f32x2(pack_u32x2(s[c + 2 * e], s[c + 2 * e + 1]), scale2, m2);
+            float x0, x1;
+            unpack_f32x2(x, x0, x1);
+            x0 = attn_exp2(x0);
+            x1 = attn_exp2(x1);
+            sum[e & 3] = add_f32x2(sum[e & 3], pack_f32x2(x0, x1));
+            if constexpr (std::is_same<T, __nv_bfloat16>::value) p[e] = pack_bf162(x0, x1);
+            else p[e] = pack_half2(x0, x1);
           }
-          // the pair (c, c + 1) goes into word c / 2
-          if constexpr (std::is_same<T, __nv_bfloat16>::value) {
-            s[c / 2] = pack_bf162(__uint_as_float(s[c]), __uint_as_float(s[c + 1]));
-            s[c / 2 + 1] = pack_bf162(__uint_as_float(s[c + 2]), __uint_as_float(s[c + 3]));
-          } else {
-            s[c / 2] = pack_half2(__uint_as_float(s[c]), __uint_as_float(s[c + 1]));
-            s[c / 2 + 1] = pack_half2(__uint_as_float(s[c + 2]), __uint_as_float(s[c + 3]));
-          }
+          tmem_st16(ts + c / 2, p);
         }
-        l_run += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-        tmem_st32(ts, s);
-        tmem_st32(ts + 32, s + 32);
+        float l0, l1;
+        unpack_f32x2(add_f32x2(add_f32x2(sum[0], sum[1]), add_f32x2(sum[2], sum[3])), l0, l1);
+        l_run += l0 + l1;
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_at(p_ready);
       }
-      // ---------------- both groups' sums, relative to the last reference
-      if (ntiles > 0 && ((step - 1) & 1) != g) {
-        const float m = receive(ok);
-        l_run *= exp2f(m_run - m);
+      // ---------------- the group whose step was not the last gives the other its sums, relative
+      // to the last reference, and goes on to the next tile, whose first step is its own
+      if (((step - 1) & 1) != g) {
+        if (ntiles > 0) {
+          const float m = receive(ok);
+          l_run *= exp2f(m_run - m);
+        }
+        if (w > 0) ok = ok && wait(&fb.l_free[quad], (w - 1) & 1);
+        fb.l_part[r] = l_run;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&fb.l_full[quad]);
+        continue;
       }
-      if (w > 0) ok = ok && wait(&fb.l_free[quad], (w - 1) & 1);
-      fb.l_part[g][r] = l_run;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&fb.l_full[quad]);
+      // ---------------- the other one reads O out: O / l, gated
       ok = ok && wait(&fb.l_full[quad], w & 1);
-      const float l = fb.l_part[0][r] + fb.l_part[1][r];
+      const float l = l_run + fb.l_part[r];
+      const float inv = a.parts > 1 ? 1.f : 1.f / l;  // used where l > 0
       __syncwarp();
       if (lane == 0) mbar_arrive(&fb.l_free[quad]);
-      const float inv = l > 0.f ? 1.f / l : 0.f;
-      // ---------------- this group's half of O / l, gated
-      const bool mine = r < tile.rows;
-      const int64_t row = tile.row0 + r;
-      const int d0 = tile.head * kD + 128 * g;
-      uint4 x[16];  // the row's gate, then its output, as 16-bit values
-      if (a.gate && mine) {
-        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T*>(a.gate) + row * a.ldg + d0);
+      // 32 rows x 64 dims at a time go through the warp's staging in fp32 (16-byte chunks
+      // XOR-swizzled by the row): in, a lane has a row; out, eight lanes have 8 dims each of one
+      // row, so gate and output rows move in whole 128-byte lines.  The loop stays a loop: its
+      // code unrolled does not fit the instruction cache beside the softmax.
+      unsigned char* mine = stage + quad * (32 * 256);
+      const int chunk = lane & 7, sub = lane >> 3;  // out: dims 8 chunk .. + 7 of rows 4 k + sub
+      const int64_t first_row = tile.row0 + quad * 32 + sub;
+      const int rows_left = tile.rows - quad * 32 - sub;
+      const T* gsrc = static_cast<const T*>(a.gate) + first_row * a.ldg + tile.head * kD + 8 * chunk;
+      T* dst = static_cast<T*>(a.out) + first_row * a.ldo + tile.head * kD + 8 * chunk;
+      const int64_t part_row = (2 * static_cast<int64_t>(tile.pair) + rank) * kFaM + quad * 32;
+      float* part = a.part_o + (part_row + sub) * kD + 8 * chunk;
+      if (a.parts > 1) a.part_ml[part_row + lane] = make_float2(m_run, l);
+      if (!ok) break;
+#pragma unroll 1
+      for (int c = 0; c < kD; c += 64) {
+        uint4 gate[8];
+        if (kGate && a.parts == 1) {
 #pragma unroll
-        for (int j = 0; j < 16; ++j) x[j] = __ldg(src + j);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 16; ++j) x[j] = make_uint4(0u, 0u, 0u, 0u);
-      }
-      ok = ok && wait(&fb.o_full, w & 1);
-      tc_fence_after();
-      // O leaves TMEM before anything is stored: the next tile's first product waits for it
-#pragma unroll
-      for (int c = 0; c < 128; c += 32) {
-        uint32_t o[32];
-        tmem_ld32(tmem_o + lanes + 128 * g + c, o);
+          for (int k = 0; k < 8; ++k)
+            gate[k] = 4 * k < rows_left ? __ldg(reinterpret_cast<const uint4*>(gsrc + 4 * k * a.ldg + c))
+                                        : make_uint4(0u, 0u, 0u, 0u);
+        }
+        if (c == 0) {
+          if (!(ok = wait(&fb.o_full, w & 1))) break;
+          tc_fence_after();
+        }
+        uint32_t o[64];
+        tmem_ld32(tmem_o + lanes + c, o);
+        tmem_ld32(tmem_o + lanes + c + 32, o + 32);
         tmem_ld_wait();
+        if (c + 64 == kD) {  // O has left TMEM: the next tile's first product may overwrite it
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_at(o_free);
+        }
+        __syncwarp();
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < 16; ++j) {
+          float4 v;  // O of a row that saw nothing may be anything
+          v.x = l > 0.f ? __uint_as_float(o[4 * j]) * inv : 0.f;
+          v.y = l > 0.f ? __uint_as_float(o[4 * j + 1]) * inv : 0.f;
+          v.z = l > 0.f ? __uint_as_float(o[4 * j + 2]) * inv : 0.f;
+          v.w = l > 0.f ? __uint_as_float(o[4 * j + 3]) * inv : 0.f;
+          *reinterpret_cast<float4*>(mine + lane * 256 + ((j ^ (lane & 15)) << 4)) = v;
+        }
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int i = 4 * k + sub;
           float y[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) y[e] = l > 0.f ? __uint_as_float(o[8 * j + e]) * inv : 0.f;
-          if (a.gate) {
+          *reinterpret_cast<float4*>(y) =
+              *reinterpret_cast<const float4*>(mine + i * 256 + (((2 * chunk) ^ (i & 15)) << 4));
+          *reinterpret_cast<float4*>(y + 4) =
+              *reinterpret_cast<const float4*>(mine + i * 256 + (((2 * chunk + 1) ^ (i & 15)) << 4));
+          if (kGate && a.parts == 1) {
             Row8<T> graw;
-            graw.a = x[c / 8 + j];
+            graw.a = gate[k];
             float gv[8];
             graw.get(gv);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] *= gate_factor(gv[e]);
+            for (int e = 0; e < 8; ++e) y[e] *= fa_gate(gv[e]);
           }
-          x[c / 8 + j] = Row8<T>::pack(y);
+          if (4 * k < rows_left) {
+            if (a.parts == 1) Row8<T>::store(dst + 4 * k * a.ldo + c, y);
+            else Row8<float>::store(part + 4 * k * kD + c, y);
+          }
         }
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_at(o_free);
-      if (mine && ok) {
-        uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(a.out) + row * a.ldo + d0);
-#pragma unroll
-        for (int j = 0; j < 16; ++j) dst[j] = x[j];
       }
     }
   }
@@ -741,6 +847,63 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFaThreads, 1)
   cluster_sync_all();  // nothing of the pair reads or signals the other CTA any more
   tc_fence_after();
   if (warp == 9) tmem2_dealloc(tmem, 512u);
+}
+
+// Joins the parts of one packed row and head by log-sum-exp: o = sum_p o_p 2^(m_p - M) over
+// sum_p l_p 2^(m_p - M).  grid: (rows_q, ceil(hq / 8)); block: 256, a warp a head.
+template <typename T>
+__global__ void __launch_bounds__(256) prompt_join_kernel(FaArgs a) {
+  const int lane = threadIdx.x & 31, row = blockIdx.x, head = blockIdx.y * 8 + (threadIdx.x >> 5);
+  griddep_wait();
+  if (head >= a.hq) return;
+  PagedBatch b;
+  b.cu = a.cu_q;
+  b.nseq = a.nseq;
+  const int s = batch_find(b, row, lane);
+  if (s < 0) return;
+  const int block_rows = a.by_heads ? kFaM : 2 * kFaM;
+  int before = 0, total = 0;
+  for (int s0 = 0; s0 < a.nseq; s0 += 32) {
+    const int nb = fa_blocks(a, s0 + lane, block_rows);
+    total += nb;
+    before += s0 + lane < s ? nb : 0;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    total += __shfl_xor_sync(0xffffffffu, total, o);
+    before += __shfl_xor_sync(0xffffffffu, before, o);
+  }
+  const int at = row - fa_bound(a.cu_q, s, a.rows_q);
+  const int idx = total - 1 - (before + at / block_rows);
+  const int sets = a.by_heads ? a.hq / 2 : a.hq, set = a.by_heads ? head / 2 : head;
+  const int rank = a.by_heads ? head & 1 : (at / kFaM) & 1;
+  float top = -INFINITY, l = 0.f, x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  for (int p = 0; p < a.parts; ++p) {
+    const int64_t pair = (static_cast<int64_t>(idx) * a.parts + p) * sets + set;
+    const int64_t r = (2 * pair + rank) * kFaM + at % kFaM;
+    const float2 ml = __ldcg(a.part_ml + r);
+    if (!(ml.y > 0.f)) continue;  // the part saw nothing (its rows hold anything)
+    const float mnew = fmaxf(top, ml.x), w = attn_exp2(ml.x - mnew), keep = attn_exp2(top - mnew);
+    top = mnew;
+    l = fmaf(l, keep, w * ml.y);
+    const float4* src = reinterpret_cast<const float4*>(a.part_o + r * kD + 8 * lane);
+    const float4 lo = __ldcg(src), hi = __ldcg(src + 1);
+    const float y[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = fmaf(x[e], keep, w * y[e]);
+  }
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) x[e] *= inv;
+  if (a.gate) {
+    Row8<T> graw;
+    graw.load(static_cast<const T*>(a.gate) + row * a.ldg + head * kD + 8 * lane);
+    float g[8];
+    graw.get(g);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] *= gate_factor(g[e]);
+  }
+  Row8<T>::store(static_cast<T*>(a.out) + row * a.ldo + head * kD + 8 * lane, x);
 }
 
 }  // namespace qsa

@@ -44,8 +44,9 @@ SIGNATURES = {
     "qsa_paged_read": (_I, [_P, _P, _I, _I, _P, _I64, _P, _I64, _P]),
     "qsa_paged_decode_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I]),
     "qsa_paged_decode": (_I, [_P, _P, _I, _I, _I, _I, _I, _P, _I64, _P, _I64, _F, _P, _SZ, _P, _I64, _P]),
-    "qsa_prompt_attn": (_I, [_I, _P, _P, _I, _I, _I, _I, _I, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _F, _P, _I64,
-                             _P]),
+    "qsa_prompt_attn_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I]),
+    "qsa_prompt_attn": (_I, [_I, _P, _P, _I, _I, _I, _I, _I, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _F, _P, _SZ, _P,
+                             _I64, _P]),
     "qsa_device_status": (_I, [_P, _P]),
     "qsa_selftest_wait_timeout": (_I, [_P]),
     "qsa_trace_begin": (_I, [_I, _P]),
@@ -475,7 +476,11 @@ def paged_decode(cache: PagedCache, batch: Batch, q, scale: float = 1 / 16, max_
     return out
 
 
-def prompt_attn(q, k, v, cu_q, cu_k=None, scale: float = 1 / 16, gate=None, out=None, stream=None):
+def prompt_attn_workspace_bytes(nseq: int, rows_q: int, rows_k: int, hq: int, hkv: int) -> int:
+    return int(load().qsa_prompt_attn_workspace_bytes(nseq, rows_q, rows_k, hq, hkv))
+
+
+def prompt_attn(q, k, v, cu_q, cu_k=None, scale: float = 1 / 16, gate=None, out=None, ws=None, stream=None):
     """Causal attention over packed prompts: q, gate, out [rows][hq][256], k, v [keys][hkv][256]
     (float16 or bfloat16, row strides free), cu_q / cu_k int32 [nseq + 1] (cu_k None: cu_q).
     Rows of no sequence are left as they were (undefined in an output allocated here)."""
@@ -502,8 +507,15 @@ def prompt_attn(q, k, v, cu_q, cu_k=None, scale: float = 1 / 16, gate=None, out=
             out = torch.empty(rows, hq, D, dtype=dtype, device=dev)
         op, ldo = _packed(out, hq, dtype, dev, "out")
         _same_rows(out, rows, "out")
-        _check(load().qsa_prompt_attn(cu_q.shape[0] - 1, cu_q.data_ptr(), cu_k.data_ptr(), rows, k.shape[0], code, hq,
-                                      hkv, qp, ldq, kp, ldk, vp, ldv, gp, ldg, scale, op, ldo, _stream(stream)))
+        lib, nseq, keys = load(), cu_q.shape[0] - 1, k.shape[0]
+        if ws is None:
+            need = lib.qsa_prompt_attn_workspace_bytes(nseq, rows, keys, hq, hkv)
+            ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+        elif ws.device != dev or not ws.is_contiguous():
+            raise ValueError(f"ws must be contiguous on {dev}")
+        _check(lib.qsa_prompt_attn(nseq, cu_q.data_ptr(), cu_k.data_ptr(), rows, keys, code, hq, hkv, qp, ldq, kp, ldk,
+                                   vp, ldv, gp, ldg, scale, _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(),
+                                   op, ldo, _stream(stream)))
     return out
 
 
