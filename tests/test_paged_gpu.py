@@ -10,6 +10,11 @@ for fp32, relative to the value.
   fp16 / bf16: the output's rounding u * |o| <= u * A, the weights' 2^-11 and the V values'
   2^-11 (V below fp16's normal range is not drawn), ex2 and fp32 sums below 2^-17, q exact in
   fp16: together u + 2 * 2^-11, with 30 % for the rest u + 2.6 * 2^-11.
+  fp16 / bf16 calls also round K = code * scale to fp16: each product q_d k_d of a score is off by
+  an independent rounding of at most 2^-11 |q_d k_d|, variance a third of its square at most, so a
+  score by 2^-11 / sqrt(3) * scale * |q o k| (the 2-norm of the products) in standard deviation; six
+  of them, for the row and cell where that is largest, bound every weight's relative error and so the
+  output's share of A.  That is added for these types.
   A weight below fp16's normal range is off by up to 2^-25 (half its subnormal step) where the
   largest weight is at least 1, whatever the weight: in a dim whose heavy cells hold codes of 0
   that is no fraction of A but up to sum_c 2^-25 |v_c| <= cells * 2^-25 * max|v|, and an fp32
@@ -136,6 +141,11 @@ def check_decode(qsa, c, hq, dtype, gated=False, max_q=None, max_len=None, scale
         err = np.abs(got[a:b] - ref)
         assert np.all(np.isfinite(got[a:b]))
         assert np.all(err[mag == 0] == 0.0)
+        if c.lens[s] and dtype != torch.float32:
+            k2 = np.square(c.values(c.k, c.ks, s, 0, c.lens[s]))
+            q2 = np.square(q[a:b].double().cpu().numpy()).reshape(b - a, c.hkv, -1, D)
+            norm = np.sqrt(max((q2[:, g].reshape(-1, D) @ k2[:, g].T).max() for g in range(c.hkv)))
+            err = np.maximum(err - 6 * 2.0 ** -11 / 3 ** 0.5 * scale * norm * mag, 0)
         if c.lens[s]:
             err = np.maximum(err - (c.lens[s] + 1) * 2.0 ** -25 * max(1.0, np.abs(c.values(c.v, c.vs, s, 0, c.lens[s])).max()), 0)
         worst = max(worst, float((err / np.maximum(mag, 1e-30)).max()))

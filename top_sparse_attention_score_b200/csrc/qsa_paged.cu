@@ -9,6 +9,7 @@
 #include "qsa_host.h"
 #include "qsa_paged_cache.cuh"
 #include "qsa_paged_decode.cuh"
+#include "qsa_paged_decode_tc.cuh"
 #include "qsa_prompt_attn.cuh"
 
 using namespace qsa::host;
@@ -91,8 +92,9 @@ cudaError_t launch_read(const qsa::PagedBatch& b, const qsa::PagedCells& c, int 
 
 // ---- decode plan
 
-// Kernel shape for a call's row tiles: the tiles of 16 query rows (warps of a group) and the
-// groups of a CTA; two CTAs per SM where registers and shared memory allow.
+// Kernel shape for a call's rows.  fp32 calls (split): the tiles of 16 query rows (warps of a
+// group) and the groups of a CTA, two CTAs per SM where registers and shared memory allow.
+// fp16 / bf16 calls: one CTA per SM, blocks of 64 cells whatever the rows.
 struct DecodePlan {
   int mt, groups, ctas_per_sm, prows, block_cells;
   int64_t blocks;  // upper bound of the flat list
@@ -104,9 +106,9 @@ DecodePlan plan_decode(int nseq, int hkv, int group, int max_q, int64_t max_len,
   DecodePlan p;
   p.mt = (max_q * group + 15) / 16;
   p.groups = p.mt == 1 ? 4 : p.mt == 2 ? 2 : 1;
-  p.ctas_per_sm = p.mt <= 3 || (p.mt == 4 && !split) ? 2 : 1;
+  p.ctas_per_sm = split && p.mt <= 3 ? 2 : 1;
   p.prows = 16 * p.mt;
-  p.block_cells = 16 * p.groups;
+  p.block_cells = split ? 16 * p.groups : qsa::kTdCells;
   p.blocks = static_cast<int64_t>(nseq) * hkv * ((max_len + p.block_cells - 1) / p.block_cells);
   p.grid = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(p.blocks, static_cast<int64_t>(sms) * p.ctas_per_sm)));
   p.part_o = 0;
@@ -130,35 +132,49 @@ int check_decode_sizes(int nseq, int hq, int hkv, int max_q, int64_t max_len) {
   return QSA_OK;
 }
 
-template <typename T, int MT, int C, int STAGES, int MINB>
-cudaError_t launch_decode_shape(const qsa::PdArgs& a, int grid, cudaStream_t s) {
-  using Smem = qsa::PdSmem<MT, C, STAGES, sizeof(T) == 4>;
-  auto kernel = qsa::paged_decode_kernel<T, MT, C, STAGES, MINB>;
-  // Opt in to the dynamic shared memory once per device.
-  static std::atomic<uint64_t> done{0};
+// Launch with the kernel's dynamic shared memory opted in to, once per device (`done`: its mask).
+template <typename K>
+cudaError_t launch_big(K kernel, std::atomic<uint64_t>& done, int grid, int threads, int smem, const qsa::PdArgs& a,
+                       cudaStream_t s) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const uint64_t bit = 1ull << (dev & 63);
   if (!(done.load(std::memory_order_relaxed) & bit)) {
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem::kBytes);
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     done.fetch_or(bit, std::memory_order_relaxed);
   }
-  return launch_pdl(kernel, dim3(grid), dim3(32 * MT * C), Smem::kBytes, s, a);
+  return launch_pdl(kernel, dim3(grid), dim3(threads), smem, s, a);
+}
+
+template <int MT, int C, int STAGES, int MINB>
+cudaError_t launch_decode_split(const qsa::PdArgs& a, int grid, cudaStream_t s) {
+  static std::atomic<uint64_t> done{0};
+  return launch_big(qsa::paged_decode_kernel<MT, C, STAGES, MINB>, done, grid, 32 * MT * C,
+                    qsa::PdSmem<MT, C, STAGES>::kBytes, a, s);
+}
+
+template <typename T>
+cudaError_t launch_decode_tc(const qsa::PdArgs& a, int grid, cudaStream_t s) {
+  static std::atomic<uint64_t> done{0};
+  return launch_big(qsa::paged_decode_tc_kernel<T>, done, grid, qsa::kTdThreads, qsa::kTdSmemBytes, a, s);
 }
 
 template <typename T>
 int launch_decode(const qsa::PdArgs& a, const DecodePlan& p, int hq, cudaStream_t s) {
-  constexpr bool split = sizeof(T) == 4;
   cudaError_t e = cudaSuccess;
-  switch (p.mt) {
-    case 1: e = launch_decode_shape<T, 1, 4, split ? 2 : 3, 2>(a, p.grid, s); break;
-    case 2: e = launch_decode_shape<T, 2, 2, 4, 2>(a, p.grid, s); break;
-    case 3: e = launch_decode_shape<T, 3, 1, 5, 2>(a, p.grid, s); break;
-    case 4: e = launch_decode_shape<T, 4, 1, 6, split ? 1 : 2>(a, p.grid, s); break;
-    case 5: e = launch_decode_shape<T, 5, 1, 8, 1>(a, p.grid, s); break;
-    default: e = launch_decode_shape<T, 6, 1, 8, 1>(a, p.grid, s); break;
+  if constexpr (sizeof(T) == 2) {
+    e = launch_decode_tc<T>(a, p.grid, s);
+  } else {
+    switch (p.mt) {
+      case 1: e = launch_decode_split<1, 4, 2, 2>(a, p.grid, s); break;
+      case 2: e = launch_decode_split<2, 2, 4, 2>(a, p.grid, s); break;
+      case 3: e = launch_decode_split<3, 1, 5, 2>(a, p.grid, s); break;
+      case 4: e = launch_decode_split<4, 1, 6, 1>(a, p.grid, s); break;
+      case 5: e = launch_decode_split<5, 1, 8, 1>(a, p.grid, s); break;
+      default: e = launch_decode_split<6, 1, 8, 1>(a, p.grid, s); break;
+    }
   }
   int r = launched("paged_decode_kernel", e);
   if (r) return r;
@@ -343,6 +359,7 @@ int qsa_paged_decode(const qsa_paged_cache* cache, const qsa_batch* batch, int r
   a.part_ml = reinterpret_cast<float2*>(base + p.part_ml);
   a.unit = reinterpret_cast<int2*>(base + p.unit);
   a.prows = p.prows;
+  a.status = device_status();
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   r = dtype == QSA_F32   ? launch_decode<float>(a, p, hq, s)
       : dtype == QSA_F16 ? launch_decode<__half>(a, p, hq, s)

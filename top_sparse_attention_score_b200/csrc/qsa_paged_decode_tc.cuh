@@ -1,0 +1,474 @@
+// qsa_paged_decode_tc.cuh -- the paged decode attention of fp16 / bf16 calls on tcgen05.
+//
+// Mathematics, flat work list and partial slots are those of qsa_paged_decode.cuh; the query
+// rows of a sequence and KV head (tokens x heads, at most 96) are rows of one 128-row tile.
+//
+// Bound: HBM.  Turning a cell's 512 codes into fp16 is what the issue slots go to (about 35 warp
+// instructions a cell of the 93 that HBM's rate leaves), and mma.sync needs them again for every
+// 16 rows and holds O in registers (8 warps an SM: 86 us for 2 x 131072 cells and one token,
+// 256 us for four).  Here sixteen warps do nothing else, the products cost no issue slots, and
+// their cost does not depend on the rows.  One CTA per SM:
+//   * sixteen warps fetch and convert: a lane loads 16 codes, makes them fp16(code * scale) and
+//     stores them into the K or V tile of 64 cells (128-byte swizzle; the same layout serves K as
+//     a K-major and V as an MN-major operand).  The loads of the next block are in flight in
+//     registers while this one converts, its cells' pages are looked up a block before that;
+//   * one thread issues S = Q K^T with Q in TMEM (so the products read each converted value from
+//     shared memory once), then O += P V with P in TMEM: 2 x 64 columns of S, 128 of Q, 256 of O;
+//   * four warps own the rows: softmax with a lagging reference maximum, the end of each piece.
+// Products of a block: 512 + 512 cycles of the tensor pipe, 16 a cell of HBM's 23.
+//
+// q enters as fp16 (bf16 q of ordinary size is exact), K and V as fp16(code * scale), the weights as
+// fp16: roundings of 2^-12 each against an output rounded to 2^-12 or 2^-9.
+#pragma once
+
+#include "qsa_paged_decode.cuh"
+#include "qsa_prompt_attn.cuh"
+
+namespace qsa {
+
+constexpr int kTdCells = 64;              // cells of a block
+constexpr int kTdTile = kTdCells * kD * 2;  // 32 KB: a converted K or V block
+constexpr int kTdStages = 2;
+constexpr int kTdConvWarps = 16;
+// Warpgroups: softmax; MMA and three idle warps; four of conversion.
+constexpr int kTdThreads = 256 + 32 * kTdConvWarps;
+constexpr int kTdRegsLaunch = 80, kTdRegsSoftmax = 128, kTdRegsMma = 64, kTdRegsConv = 72;
+static_assert(kTdRegsSoftmax + kTdRegsMma + 4 * kTdRegsConv <= 6 * kTdRegsLaunch, "registers of the launch");
+static_assert(kTdRegsSoftmax > kTdRegsLaunch && kTdRegsMma < kTdRegsLaunch && kTdRegsConv < kTdRegsLaunch,
+              "which groups grow and which shrink");
+
+struct __align__(16) TdBarriers {
+  uint64_t k_full[kTdStages], k_empty[kTdStages];
+  uint64_t v_full[kTdStages], v_empty[kTdStages];
+  uint64_t s_full[2], p_ready[2];
+  uint64_t q_ready;   // one phase per piece: its Q is in TMEM
+  uint64_t pv_done;   // one phase per block
+  uint64_t o_full, o_free;  // one phase per piece
+  uint64_t drain;
+  uint8_t valid[4][8];  // block % 4: bit c of the 64 is set when cell c exists
+  uint32_t tmem_base;
+  uint32_t abort;
+};
+constexpr int kTdSmemBytes = 1024 + 2 * kTdStages * kTdTile + static_cast<int>(sizeof(TdBarriers));
+
+// Walks the flat list: block f of it is block `blk` of the unit (seq, kvh).
+struct TdWalk {
+  int seq, before, nb;  // sequence, blocks in front of it, its blocks per KV head
+  PdSeq q;
+  int kvh, blk;
+};
+
+__device__ __forceinline__ int td_blocks(const PdSeq& q) { return (q.cells + kTdCells - 1) / kTdCells; }
+
+// To block f of the flat list, within the walk's sequence.
+__device__ __forceinline__ void td_open(TdWalk& w, int f) {
+  w.kvh = (f - w.before) / w.nb;
+  w.blk = (f - w.before) - w.kvh * w.nb;
+}
+
+// To the next block of the flat list, which has one; true where it begins a unit.
+__device__ __forceinline__ bool td_next(const PdArgs& a, TdWalk& w) {
+  if (++w.blk < w.nb) return false;
+  w.blk = 0;
+  if (++w.kvh < a.c.hkv) return true;
+  w.kvh = 0;
+  do {  // sequences without cells have no blocks
+    w.q = pd_seq(a, ++w.seq);
+    w.nb = td_blocks(w.q);
+  } while (w.nb == 0);
+  return true;
+}
+
+// 16 codes as fp16(code * scale): two 16-byte chunks.
+__device__ __forceinline__ void td_convert16(const uint4& codes, __half2 scale, uint4& lo, uint4& hi) {
+  const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
+  uint32_t r[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t x = w[i] ^ 0x80808080u;
+    const uint32_t a = i8x2_to_h2(x, 0x4140u), b = i8x2_to_h2(x, 0x4342u);
+    const __half2 ha = __hmul2(*reinterpret_cast<const __half2*>(&a), scale);
+    const __half2 hb = __hmul2(*reinterpret_cast<const __half2*>(&b), scale);
+    r[2 * i] = *reinterpret_cast<const uint32_t*>(&ha);
+    r[2 * i + 1] = *reinterpret_cast<const uint32_t*>(&hb);
+  }
+  lo = make_uint4(r[0], r[1], r[2], r[3]);
+  hi = make_uint4(r[4], r[5], r[6], r[7]);
+}
+
+// grid: CTAs that share the flat block list; block: 768; dynamic shared memory: kTdSmemBytes.
+template <typename T>
+__global__ void __launch_bounds__(kTdThreads, 1) paged_decode_tc_kernel(PdArgs a) {
+  constexpr uint32_t kIdescQK = umma_idesc_f16(128, kTdCells, false, false);
+  constexpr uint32_t kIdescPV = umma_idesc_f16(128, kD, false, true);
+  extern __shared__ unsigned char td_raw[];
+  unsigned char* smem =
+      reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(td_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  unsigned char* sk = smem;
+  unsigned char* sv = smem + kTdStages * kTdTile;
+  TdBarriers& tb = *reinterpret_cast<TdBarriers*>(smem + 2 * kTdStages * kTdTile);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int hkv = a.c.hkv;
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, fa_wait(bar, parity, &tb.abort, a.status)) != 0;
+  };
+
+  griddep_wait();
+  // ---- this CTA's range of the flat list, and where it starts (every warp the same)
+  int total = 0;
+  for (int s0 = 0; s0 < a.b.nseq; s0 += 32) {
+    const int s = s0 + lane;
+    total += s < a.b.nseq ? td_blocks(pd_seq(a, s)) : 0;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  total *= hkv;
+  const int per = max(1, (total + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x));
+  const int from = min(total, static_cast<int>(blockIdx.x) * per), to = min(total, from + per);
+  griddep_launch();  // the join waits for this grid before it reads anything
+  if (from >= to) return;
+  TdWalk walk;
+  walk.seq = 0;
+  walk.before = 0;
+  for (int s0 = 0, base = 0; s0 < a.b.nseq; s0 += 32) {
+    const int s = s0 + lane;
+    const int nb = s < a.b.nseq ? td_blocks(pd_seq(a, s)) * hkv : 0;
+    int inc = nb;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += y;
+    }
+    const uint32_t past = __ballot_sync(0xffffffffu, base + inc > from);
+    if (past) {
+      const int l = __ffs(past) - 1;
+      walk.seq = s0 + l;
+      walk.before = base + __shfl_sync(0xffffffffu, inc - nb, l);
+      break;
+    }
+    base += __shfl_sync(0xffffffffu, inc, 31);
+  }
+  walk.q = pd_seq(a, walk.seq);
+  walk.nb = td_blocks(walk.q);
+  td_open(walk, from);
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kTdStages; ++i) {
+      mbar_init(&tb.k_full[i], kTdConvWarps / 2);
+      mbar_init(&tb.v_full[i], kTdConvWarps / 2);
+      mbar_init(&tb.k_empty[i], 1);
+      mbar_init(&tb.v_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&tb.s_full[i], 1);
+      mbar_init(&tb.p_ready[i], 4);
+    }
+    mbar_init(&tb.q_ready, 4);
+    mbar_init(&tb.pv_done, 1);
+    mbar_init(&tb.o_full, 1);
+    mbar_init(&tb.o_free, 4);
+    mbar_init(&tb.drain, 1);
+    tb.abort = 0u;
+    mbar_init_fence();
+  }
+  if (warp == 4) tmem_alloc(&tb.tmem_base, 512u);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tb.tmem_base;
+  const uint32_t tmem_q = tmem + 2 * kTdCells, tmem_o = tmem + 256;
+  const int nblocks = to - from;
+
+  if (warp >= 8) {
+    regs_shrink<kTdRegsConv>();
+    // ---------------- conversion: warps 0..7 of it K, 8..15 V; eight cells of each block
+    const int cw = warp - 8, part = cw & 7;
+    const bool is_v = cw >= 8;
+    const int sub = lane >> 2, j = lane & 3;  // cell 8 part + sub; 16-code chunk j of each 64 dims
+    const int c = 8 * part + sub;
+    const int8_t* codes = is_v ? a.c.v : a.c.k;
+    const __half* scales = is_v ? a.c.vs : a.c.ks;
+    unsigned char* tiles = (is_v ? sv : sk) + c * 128;
+    uint64_t* full = is_v ? tb.v_full : tb.k_full;
+    uint64_t* empty = is_v ? tb.v_empty : tb.k_empty;
+    // The lane's cell of the walk's block: page table entry and offset, kept up by addition.
+    int entry = 0, off = 0;
+    auto open_page = [&]() {
+      const int p = walk.blk * kTdCells + c;
+      entry = p / a.b.page_cells;
+      off = p - entry * a.b.page_cells;
+    };
+    open_page();
+    int at = 0;  // block of the walk
+    // row of the cell arrays of this lane's cell of the next block; -1: none
+    auto lookup = [&]() {
+      if (at >= nblocks) return static_cast<int64_t>(-1);
+      int page = -1;
+      if (walk.blk * kTdCells + c < walk.q.cells && entry < a.b.table_ld)
+        page = __ldg(a.b.table + static_cast<size_t>(walk.seq) * a.b.table_ld + entry);
+      const int64_t row = page < 0 || page >= a.b.pages
+                              ? static_cast<int64_t>(-1)
+                              : static_cast<int64_t>(page * a.b.page_cells + off) * hkv + walk.kvh;
+      if (++at < nblocks) {
+        if (td_next(a, walk)) {
+          open_page();
+        } else {
+          off += kTdCells;
+          while (off >= a.b.page_cells) off -= a.b.page_cells, ++entry;
+        }
+      }
+      return row;
+    };
+    struct Loaded {
+      uint4 code[4];
+      uint4 scale;
+      bool there;
+    };
+    auto load = [&](Loaded& x, int64_t row) {
+      x.there = row >= 0;
+      const int8_t* src = codes + row * kD + 16 * j;
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        x.code[u] = x.there ? __ldg(reinterpret_cast<const uint4*>(src + 64 * u)) : make_uint4(0u, 0u, 0u, 0u);
+      x.scale = x.there ? __ldg(reinterpret_cast<const uint4*>(scales + row * kNG)) : make_uint4(0u, 0u, 0u, 0u);
+    };
+    bool ok = true;
+    auto convert = [&](const Loaded& x, int i) {
+      const int st = i % kTdStages;
+      ok = ok && wait(empty + st, ((i / kTdStages) & 1) ^ 1);
+      unsigned char* dst = tiles + st * kTdTile;
+      const uint32_t sc[4] = {x.scale.x, x.scale.y, x.scale.z, x.scale.w};
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        // group of the lane's 16 dims: 2 u + (j >> 1)
+        const __half2 pair = *reinterpret_cast<const __half2*>(&sc[u]);
+        uint4 lo, hi;
+        td_convert16(x.code[u], (j >> 1) ? __high2half2(pair) : __low2half2(pair), lo, hi);
+        *reinterpret_cast<uint4*>(dst + u * (kTdCells * 128) + (((2 * j) ^ sub) << 4)) = lo;
+        *reinterpret_cast<uint4*>(dst + u * (kTdCells * 128) + (((2 * j + 1) ^ sub) << 4)) = hi;
+      }
+      if (!is_v) {
+        const bool cell_there = __shfl_sync(0xffffffffu, x.there, (lane & 7) << 2);  // of cell lane % 8
+        const uint32_t m = __ballot_sync(0xffffffffu, cell_there);
+        if (lane == 0) tb.valid[i & 3][part] = static_cast<uint8_t>(m);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(full + st);
+    };
+    Loaded x[2];
+    int64_t row = lookup(), next = lookup();
+    load(x[0], row);
+    for (int i = 0; i < nblocks; i += 2) {
+      row = next;
+      next = lookup();
+      load(x[1], row);
+      convert(x[0], i);
+      if (i + 1 >= nblocks) break;
+      row = next;
+      next = lookup();
+      load(x[0], row);
+      convert(x[1], i + 1);
+    }
+  } else if (warp >= 4) {
+    regs_shrink<kTdRegsMma>();
+    if (warp == 4 && lane == 0) {
+      // ---------------- MMA: S of block i + 1 goes ahead of the product of block i
+      bool ok = true;
+      const uint32_t k0 = smem_u32(sk), v0 = smem_u32(sv);
+      auto wait1 = [&](uint64_t* bar, uint32_t parity) { return ok = fa_wait(bar, parity, &tb.abort, a.status); };
+      TdWalk ahead = walk;
+      int pieces_q = 0, pieces_o = 0;  // pieces whose Q was awaited, whose O was begun
+      auto scores = [&](int i) {
+        const bool opens = i == 0 || td_next(a, ahead);
+        if (opens && !wait1(&tb.q_ready, pieces_q++ & 1)) return;
+        const int st = i % kTdStages;
+        if (!wait1(&tb.k_full[st], (i / kTdStages) & 1)) return;
+        tc_fence_after();
+#pragma unroll 4
+        for (int ks = 0; ks < 16; ++ks)
+          umma_f16_ts(tmem + (i & 1) * kTdCells, tmem_q + ks * 8,
+                      umma_desc_k_sw128(k0 + st * kTdTile + (ks >> 2) * (kTdCells * 128) + (ks & 3) * 32, 1024),
+                      kIdescQK, ks > 0 ? 1u : 0u);
+        umma_commit(&tb.k_empty[st]);
+        umma_commit(&tb.s_full[i & 1]);
+      };
+      scores(0);
+      for (int i = 0; i < nblocks && ok; ++i) {
+        if (i + 1 < nblocks) scores(i + 1);
+        if (!ok) break;
+        const bool first = i == 0 || td_next(a, walk), last = i + 1 == nblocks || walk.blk + 1 == walk.nb;
+        // the last piece's O must have been read out
+        if (first && pieces_o++ > 0 && !wait1(&tb.o_free, (pieces_o - 2) & 1)) break;
+        const int st = i % kTdStages;
+        if (!wait1(&tb.p_ready[i & 1], (i >> 1) & 1) || !wait1(&tb.v_full[st], (i / kTdStages) & 1)) break;
+        tc_fence_after();
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks)
+          umma_f16_ts(tmem_o, tmem + (i & 1) * kTdCells + ks * 8,
+                      umma_desc_mn_sw128(v0 + st * kTdTile + ks * 2048, kTdCells * 128, 1024), kIdescPV,
+                      first && ks == 0 ? 0u : 1u);
+        umma_commit(&tb.v_empty[st]);
+        umma_commit(&tb.pv_done);
+        if (last) umma_commit(&tb.o_full);
+      }
+      umma_commit(&tb.drain);  // every MMA issued has completed once it fires
+      mbar_drain_wait(&tb.drain, 0);
+    }
+    __syncwarp();
+  } else {
+    regs_grow<kTdRegsSoftmax>();
+    // ---------------- softmax and the ends of pieces: thread = row = TMEM lane
+    const int r = warp * 32 + lane;
+    const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
+    bool ok = true;
+    int i = 0;
+    // Q of the walk's unit into TMEM: this thread's row, 0 behind the last
+    auto put_q = [&]() {
+      const int nrow = min(walk.q.n, a.max_q) * a.group;
+      const int tok = r / a.group, head = walk.kvh * a.group + r - tok * a.group;
+      const T* src = static_cast<const T*>(a.q) + (walk.q.row0 + tok) * a.ldq + head * kD;
+#pragma unroll 1
+      for (int c = 0; c < kD; c += 32) {
+        uint32_t w[16];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+          if (r < nrow) {
+            Row8<T> raw;
+            raw.load(src + c + 8 * u);
+            raw.get(x);
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) w[4 * u + e] = pack_half2(x[2 * e], x[2 * e + 1]);
+        }
+        tmem_st16(tmem_q + lanes + c / 2, w);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&tb.q_ready);
+    };
+    put_q();
+    for (int piece = 0; i < nblocks; ++piece) {
+      const PdSeq q = walk.q;
+      const int kvh = walk.kvh, unit = walk.seq * hkv + kvh, nb = walk.nb;
+      const int u0 = from + i - walk.blk;  // the unit's first block in the flat list
+      const int blk0 = walk.blk, blk1 = min(nb, to - u0);
+      const int first_cta = u0 / per, pieces = (u0 + nb - 1) / per - first_cta + 1;
+      if (blk0 == 0 && threadIdx.x == 0) a.unit[unit] = make_int2(first_cta, pieces);
+      const int nrow = min(q.n, a.max_q) * a.group;
+      const int vis = pd_visible(q, min(r / a.group, q.n - 1));  // cells that this row sees
+      float m_run = kFaNoMax, l_run = 0.f;
+      for (int blk = blk0; blk < blk1; ++blk, ++i) {
+        const uint32_t ts = tmem + lanes + (i & 1) * kTdCells;
+        ok = ok && wait(&tb.s_full[i & 1], (i >> 1) & 1);
+        tc_fence_after();
+        if (warp * 32 < nrow) {
+          uint32_t s[64];
+          tmem_ld32(ts, s);
+          tmem_ld32(ts + 32, s + 32);
+          const uint2 valid = *reinterpret_cast<const uint2*>(tb.valid[i & 3]);
+          tmem_ld_wait();
+          const int left = vis - blk * kTdCells;  // columns below this are seen
+          if (__any_sync(0xffffffffu, left < kTdCells) || (valid.x & valid.y) != 0xffffffffu) {
+#pragma unroll
+            for (int c = 0; c < 64; ++c)
+              if (c >= left || !(((c < 32 ? valid.x : valid.y) >> (c & 31)) & 1u)) s[c] = 0xff800000u;
+          }
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int c = 0; c < 64; c += 8)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              mx[e] = fmaxf(mx[e], fmaxf(__uint_as_float(s[c + e]), __uint_as_float(s[c + e + 4])));
+          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
+          if (__any_sync(0xffffffffu, top > m_run + kFaShift)) {
+            const float mnew = top > m_run + kFaShift ? top : m_run;
+            const float alpha = attn_exp2(m_run - mnew);
+            m_run = mnew;
+            l_run *= alpha;
+            if (blk > blk0) {  // O of this warp's rows, once the product of the block before is in
+              ok = ok && wait(&tb.pv_done, (i - 1) & 1);
+              tc_fence_after();
+#pragma unroll 1
+              for (int c = 0; c < kD; c += 32) {
+                uint32_t o[32];
+                tmem_ld32(tmem_o + lanes + c, o);
+                tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                tmem_st32(tmem_o + lanes + c, o);
+              }
+              tmem_st_wait();
+            }
+          }
+          const uint64_t scale2 = pack_f32x2(a.scale_log2, a.scale_log2), m2 = pack_f32x2(-m_run, -m_run);
+          uint64_t sum[2] = {0ull, 0ull};
+#pragma unroll
+          for (int c = 0; c < 64; c += 32) {
+            uint32_t p[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              float x0, x1;
+              unpack_f32x2(fma_f32x2(pack_u32x2(s[c + 2 * e], s[c + 2 * e + 1]), scale2, m2), x0, x1);
+              x0 = attn_exp2(x0);
+              x1 = attn_exp2(x1);
+              sum[e & 1] = add_f32x2(sum[e & 1], pack_f32x2(x0, x1));
+              p[e] = pack_half2(x0, x1);
+            }
+            tmem_st16(ts + c / 2, p);
+          }
+          float l0, l1;
+          unpack_f32x2(add_f32x2(sum[0], sum[1]), l0, l1);
+          l_run += l0 + l1;
+          tmem_st_wait();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&tb.p_ready[i & 1]);
+      }
+      // the next piece's Q: the scores of this one's last block are complete
+      if (i < nblocks) {
+        walk.blk = blk1 - 1;
+        td_next(a, walk);
+        put_q();
+      }
+      // ---------------- the piece's rows: final, or a partial
+      ok = ok && wait(&tb.o_full, piece & 1);
+      tc_fence_after();
+      const float inv = l_run > 0.f ? 1.f / l_run : 0.f;
+      const int tok = r / a.group, head = kvh * a.group + r - tok * a.group;
+      const size_t slot_row = (2 * static_cast<size_t>(blockIdx.x) + (blk0 == 0 ? 1 : 0)) * a.prows + r;
+      if (warp * 32 < nrow) {
+#pragma unroll 1
+        for (int c = 0; c < kD; c += 32) {
+          uint32_t o[32];
+          tmem_ld32(tmem_o + lanes + c, o);
+          tmem_ld_wait();
+          if (r < nrow && ok) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              float x[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) x[e] = l_run > 0.f ? __uint_as_float(o[8 * u + e]) : 0.f;
+              if (pieces == 1) pd_write8<T>(a, q.row0 + tok, head, c + 8 * u, x, inv);
+              else Row8<float>::store(a.part_o + slot_row * kD + c + 8 * u, x);
+            }
+          }
+          __syncwarp();
+        }
+        if (pieces > 1 && r < nrow) a.part_ml[slot_row] = make_float2(l_run > 0.f ? m_run : -INFINITY, l_run);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&tb.o_free);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 4) tmem_dealloc(tmem, 512u);
+}
+
+}  // namespace qsa
