@@ -92,11 +92,14 @@ cudaError_t launch_read(const qsa::PagedBatch& b, const qsa::PagedCells& c, int 
 
 // ---- decode plan
 
-// Kernel shape for a call's rows.  fp32 calls (split): the tiles of 16 query rows (warps of a
-// group) and the groups of a CTA, two CTAs per SM where registers and shared memory allow.
-// fp16 / bf16 calls: one CTA per SM, blocks of 64 cells whatever the rows.
+// Kernel shape for a call's rows.  fp32 calls (split), and fp16 / bf16 calls of at most 16 rows:
+// the tiles of 16 query rows (warps of a group) and the groups of a CTA, two CTAs per SM where
+// registers and shared memory allow.  fp16 / bf16 calls of more rows: the tcgen05 kernel, one CTA
+// per SM, blocks of 64 cells whatever the rows.  2 x 131072 cells of 2 KV heads, 12 rows a token:
+// one token 86 us on the first and 119 on the second, two 147 and 119, eight 491 and 128.
 struct DecodePlan {
   int mt, groups, ctas_per_sm, prows, block_cells;
+  bool tc;  // the tcgen05 kernel
   int64_t blocks;  // upper bound of the flat list
   int grid;
   size_t part_o, part_ml, unit, total;
@@ -106,9 +109,10 @@ DecodePlan plan_decode(int nseq, int hkv, int group, int max_q, int64_t max_len,
   DecodePlan p;
   p.mt = (max_q * group + 15) / 16;
   p.groups = p.mt == 1 ? 4 : p.mt == 2 ? 2 : 1;
-  p.ctas_per_sm = split && p.mt <= 3 ? 2 : 1;
+  p.tc = !split && p.mt > 1;
+  p.ctas_per_sm = !p.tc && p.mt <= 3 ? 2 : 1;
   p.prows = 16 * p.mt;
-  p.block_cells = split ? 16 * p.groups : qsa::kTdCells;
+  p.block_cells = p.tc ? qsa::kTdCells : 16 * p.groups;
   p.blocks = static_cast<int64_t>(nseq) * hkv * ((max_len + p.block_cells - 1) / p.block_cells);
   p.grid = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(p.blocks, static_cast<int64_t>(sms) * p.ctas_per_sm)));
   p.part_o = 0;
@@ -148,11 +152,11 @@ cudaError_t launch_big(K kernel, std::atomic<uint64_t>& done, int grid, int thre
   return launch_pdl(kernel, dim3(grid), dim3(threads), smem, s, a);
 }
 
-template <int MT, int C, int STAGES, int MINB>
-cudaError_t launch_decode_split(const qsa::PdArgs& a, int grid, cudaStream_t s) {
+template <typename T, int MT, int C, int STAGES, int MINB>
+cudaError_t launch_decode_mma(const qsa::PdArgs& a, int grid, cudaStream_t s) {
   static std::atomic<uint64_t> done{0};
-  return launch_big(qsa::paged_decode_kernel<MT, C, STAGES, MINB>, done, grid, 32 * MT * C,
-                    qsa::PdSmem<MT, C, STAGES>::kBytes, a, s);
+  return launch_big(qsa::paged_decode_kernel<T, MT, C, STAGES, MINB>, done, grid, 32 * MT * C,
+                    qsa::PdSmem<MT, C, STAGES, sizeof(T) == 4>::kBytes, a, s);
 }
 
 template <typename T>
@@ -165,15 +169,15 @@ template <typename T>
 int launch_decode(const qsa::PdArgs& a, const DecodePlan& p, int hq, cudaStream_t s) {
   cudaError_t e = cudaSuccess;
   if constexpr (sizeof(T) == 2) {
-    e = launch_decode_tc<T>(a, p.grid, s);
+    e = p.tc ? launch_decode_tc<T>(a, p.grid, s) : launch_decode_mma<T, 1, 4, 3, 2>(a, p.grid, s);
   } else {
     switch (p.mt) {
-      case 1: e = launch_decode_split<1, 4, 2, 2>(a, p.grid, s); break;
-      case 2: e = launch_decode_split<2, 2, 4, 2>(a, p.grid, s); break;
-      case 3: e = launch_decode_split<3, 1, 5, 2>(a, p.grid, s); break;
-      case 4: e = launch_decode_split<4, 1, 6, 1>(a, p.grid, s); break;
-      case 5: e = launch_decode_split<5, 1, 8, 1>(a, p.grid, s); break;
-      default: e = launch_decode_split<6, 1, 8, 1>(a, p.grid, s); break;
+      case 1: e = launch_decode_mma<T, 1, 4, 2, 2>(a, p.grid, s); break;
+      case 2: e = launch_decode_mma<T, 2, 2, 4, 2>(a, p.grid, s); break;
+      case 3: e = launch_decode_mma<T, 3, 1, 5, 2>(a, p.grid, s); break;
+      case 4: e = launch_decode_mma<T, 4, 1, 6, 1>(a, p.grid, s); break;
+      case 5: e = launch_decode_mma<T, 5, 1, 8, 1>(a, p.grid, s); break;
+      default: e = launch_decode_mma<T, 6, 1, 8, 1>(a, p.grid, s); break;
     }
   }
   int r = launched("paged_decode_kernel", e);

@@ -1,5 +1,5 @@
 // qsa_paged_decode.cuh -- attention of a sequence's newest tokens over all its cells in a
-// paged int8 K/V cache, split over the cells and joined: the fp32 kernel, and the join of both.
+// paged int8 K/V cache, split over the cells and joined.
 //
 // Mathematics: s_c = scale * sum_g ks[c][g] * (sum_{d in g} q[d] code_k[c][d]), an online softmax
 // (running maximum m, sum l, unnormalised o), o += p_c * vs[c][g] * code_v[c][d]; pieces of a
@@ -20,11 +20,11 @@
 //  * Cells arrive by cp.async in a ring of 16-cell stages a group owns (only its MT warps wait
 //    for it).  Rows are 256 bytes without padding; 32-byte pairs of chunks are XOR-swizzled by
 //    the cell, so the fragment reads (8 bytes of 4 cells, 4 bytes of 4 cell pairs) hit all banks.
-//  * Codes become fp16 exactly (byte permute into 0x64xx, minus 1152) and feed mma.sync m16n8k16,
-//    the K scales multiply fp32 partial scores.  q, the weights and code * vs are each a sum of two
-//    fp16 values, hi + lo, and the products hi hi + hi lo + lo hi are kept, so what is lost is
-//    2^-22: the tensor cores' other forms have no product this exact, which is why fp32 calls
-//    have a kernel of their own (fp16 / bf16: qsa_paged_decode_tc.cuh).
+//  * Codes become fp16 exactly (byte permute into 0x64xx, minus 1152) and feed mma.sync m16n8k16.
+//    fp16 / bf16 calls: q enters as fp16 (bf16 q of ordinary size is exact), V as fp16(code * vs) and the
+//    weights as fp16: two roundings of 2^-12 against an output rounded to 2^-12 or 2^-9.
+//    fp32 calls (kSplit): q, the weights and code * vs are each a sum of two fp16 values, hi + lo,
+//    and the products hi hi + hi lo + lo hi are kept, so what is lost is 2^-22.
 #pragma once
 
 #include "qsa_attn.cuh"
@@ -84,6 +84,15 @@ __device__ __forceinline__ PdSeq pd_seq(const PdArgs& a, int s) {
 // Cells that row j of the sequence sees (its last visible position + 1).
 __device__ __forceinline__ int pd_visible(const PdSeq& q, int j) { return q.len - q.n + 1 + j; }
 
+template <typename T>
+__device__ __forceinline__ float pd_to_float(T x);
+template <>
+__device__ __forceinline__ float pd_to_float(float x) { return x; }
+template <>
+__device__ __forceinline__ float pd_to_float(__half x) { return __half2float(x); }
+template <>
+__device__ __forceinline__ float pd_to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
+
 // x = hi + lo with both in fp16 (lo holds the next 11 bits).
 __device__ __forceinline__ void pd_split2(float x, float y, uint32_t& hi, uint32_t& lo) {
   const __half2 h = __floats2half2_rn(x, y);
@@ -112,21 +121,22 @@ __device__ __forceinline__ void pd_write8(const PdArgs& a, int row, int head, in
   Row8<T>::store(static_cast<T*>(a.out) + row * a.ldo + head * kD + d, x);
 }
 
-template <int MT, int C, int STAGES>
+template <int MT, int C, int STAGES, bool kSplit>
 struct PdSmem {
   static constexpr int kStageBytes = C * STAGES * static_cast<int>(sizeof(PdStage));
   static constexpr int kJoinBytes = C * MT * 16 * (kD + 4) * 4;  // rows padded to 260 floats
-  static constexpr int kQBytes = MT * 16 * kD * 4;  // hi and lo
+  static constexpr int kQBytes = MT * 16 * kD * 2 * (kSplit ? 2 : 1);
   static constexpr int kStatBytes = C * MT * 16 * 8;
   static constexpr int kBytes = kQBytes + kStatBytes + (kStageBytes > kJoinBytes ? kStageBytes : kJoinBytes);
 };
 
 // grid: CTAs that share the flat block list; block: 32 * MT * C.
-template <int MT, int C, int STAGES, int MINB>
+template <typename T, int MT, int C, int STAGES, int MINB>
 __global__ void __launch_bounds__(32 * MT * C, MINB) paged_decode_kernel(PdArgs a) {
+  constexpr bool kSplit = sizeof(T) == 4;
   constexpr int NT = 32 * MT * C, GT = 32 * MT;  // threads of the CTA, of a group
   constexpr int CB = 16 * C;                     // cells of a block of the flat list
-  using Smem = PdSmem<MT, C, STAGES>;
+  using Smem = PdSmem<MT, C, STAGES, kSplit>;
   extern __shared__ __align__(16) unsigned char smem_raw[];
   uint4* sq = reinterpret_cast<uint4*>(smem_raw);  // [MT][hi, lo][16 k-steps][32 lanes]
   float2* sstat = reinterpret_cast<float2*>(smem_raw + Smem::kQBytes);
@@ -237,16 +247,21 @@ __global__ void __launch_bounds__(32 * MT * C, MINB) paged_decode_kernel(PdArgs 
         float x[4] = {0.f, 0.f, 0.f, 0.f};
         if (r < nrow) {
           const int tok = r / a.group, head = kvh * a.group + r - tok * a.group;
-          const float4 v = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(a.q) +
-                                                                 (q.row0 + tok) * a.ldq + head * kD + d0));
-          x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+          const T* src = static_cast<const T*>(a.q) + (q.row0 + tok) * a.ldq + head * kD + d0;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x[i] = pd_to_float(src[i]);
         }
-        pd_split2(x[0], x[1], hi[h], lo[h]);
-        pd_split2(x[2], x[3], hi[h + 2], lo[h + 2]);
+        if constexpr (kSplit) {
+          pd_split2(x[0], x[1], hi[h], lo[h]);
+          pd_split2(x[2], x[3], hi[h + 2], lo[h + 2]);
+        } else {
+          hi[h] = pack_half2(x[0], x[1]);
+          hi[h + 2] = pack_half2(x[2], x[3]);
+        }
       }
-      uint4* dst = sq + (m * 2 * 16 + ks) * 32 + l;
+      uint4* dst = sq + (m * (kSplit ? 2 : 1) * 16 + ks) * 32 + l;
       dst[0] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-      dst[16 * 32] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      if constexpr (kSplit) dst[16 * 32] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
     }
     // cells that the thread's two rows see, and that every row of the tile sees
     int vis[2];
@@ -263,7 +278,7 @@ __global__ void __launch_bounds__(32 * MT * C, MINB) paged_decode_kernel(PdArgs 
       for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int c = 0; c < 4; ++c) o[gi][i][c] = 0.f;
-    const uint4* mq = sq + mt * 2 * 16 * 32 + lane;
+    const uint4* mq = sq + mt * (kSplit ? 2 : 1) * 16 * 32 + lane;
 
     int slot = 0;
     for (int blk = blk0; blk < blk1; ++blk) {
@@ -299,8 +314,12 @@ __global__ void __launch_bounds__(32 * MT * C, MINB) paged_decode_kernel(PdArgs 
       for (int qg = 0; qg < kNG; ++qg) {
         const uint4 qa = mq[(2 * qg) * 32], qb = mq[(2 * qg + 1) * 32];
         const uint32_t a0[4] = {qa.x, qa.y, qa.z, qa.w}, a1[4] = {qb.x, qb.y, qb.z, qb.w};
-        const uint4 la = mq[(16 + 2 * qg) * 32], lb = mq[(16 + 2 * qg + 1) * 32];
-        const uint32_t c0[4] = {la.x, la.y, la.z, la.w}, c1[4] = {lb.x, lb.y, lb.z, lb.w};
+        uint32_t c0[4], c1[4];
+        if constexpr (kSplit) {
+          const uint4 la = mq[(16 + 2 * qg) * 32], lb = mq[(16 + 2 * qg + 1) * 32];
+          c0[0] = la.x, c0[1] = la.y, c0[2] = la.z, c0[3] = la.w;
+          c1[0] = lb.x, c1[1] = lb.y, c1[2] = lb.z, c1[3] = lb.w;
+        }
 #pragma unroll
         for (int nt = 0; nt < 2; ++nt) {
           const uint2 kw = *reinterpret_cast<const uint2*>(st.k + pd_koff(8 * nt + g, 32 * qg + 8 * t));
@@ -308,8 +327,10 @@ __global__ void __launch_bounds__(32 * MT * C, MINB) paged_decode_kernel(PdArgs 
           const uint32_t b00 = i8x2_to_h2(x0, 0x4140u), b01 = i8x2_to_h2(x0, 0x4342u);
           const uint32_t b10 = i8x2_to_h2(x1, 0x4140u), b11 = i8x2_to_h2(x1, 0x4342u);
           float acc[4] = {0.f, 0.f, 0.f, 0.f};
-          mma_f16_16816(acc, c0, b00, b01);
-          mma_f16_16816(acc, c1, b10, b11);
+          if constexpr (kSplit) {
+            mma_f16_16816(acc, c0, b00, b01);
+            mma_f16_16816(acc, c1, b10, b11);
+          }
           mma_f16_16816(acc, a0, b00, b01);
           mma_f16_16816(acc, a1, b10, b11);
           const uint32_t wa = (&ksw[nt][0].x)[qg >> 1], wb = (&ksw[nt][1].x)[qg >> 1];
@@ -370,10 +391,17 @@ __global__ void __launch_bounds__(32 * MT * C, MINB) paged_decode_kernel(PdArgs 
 
       // ---- P V: k-index j of P is cell j
       uint32_t ph[4], pl[4];
-      pd_split2(s[0][0], s[0][1], ph[0], pl[0]);
-      pd_split2(s[0][2], s[0][3], ph[1], pl[1]);
-      pd_split2(s[1][0], s[1][1], ph[2], pl[2]);
-      pd_split2(s[1][2], s[1][3], ph[3], pl[3]);
+      if constexpr (kSplit) {
+        pd_split2(s[0][0], s[0][1], ph[0], pl[0]);
+        pd_split2(s[0][2], s[0][3], ph[1], pl[1]);
+        pd_split2(s[1][0], s[1][1], ph[2], pl[2]);
+        pd_split2(s[1][2], s[1][3], ph[3], pl[3]);
+      } else {
+        ph[0] = pack_half2(s[0][0], s[0][1]);
+        ph[1] = pack_half2(s[0][2], s[0][3]);
+        ph[2] = pack_half2(s[1][0], s[1][1]);
+        ph[3] = pack_half2(s[1][2], s[1][3]);
+      }
       uint4 vsw[4];  // the scales of cells 2t, 2t+1, 2t+8, 2t+9
 #pragma unroll
       for (int j = 0; j < 4; ++j)
@@ -399,11 +427,13 @@ __global__ void __launch_bounds__(32 * MT * C, MINB) paged_decode_kernel(PdArgs 
           const __half2 f0 = *reinterpret_cast<const __half2*>(&b0), f1 = *reinterpret_cast<const __half2*>(&b1);
           const __half2 h0 = __hmul2(f0, sAB), h1 = __hmul2(f1, sCD);
           const uint32_t v0 = *reinterpret_cast<const uint32_t*>(&h0), v1 = *reinterpret_cast<const uint32_t*>(&h1);
-          // code * vs - fp16(code * vs), exact by the fused multiply-add
-          const __half2 r0 = __hfma2(f0, sAB, __hneg2(h0)), r1 = __hfma2(f1, sCD, __hneg2(h1));
-          mma_f16_16816(o[gi][i], ph, *reinterpret_cast<const uint32_t*>(&r0),
-                        *reinterpret_cast<const uint32_t*>(&r1));
-          mma_f16_16816(o[gi][i], pl, v0, v1);
+          if constexpr (kSplit) {
+            // code * vs - fp16(code * vs), exact by the fused multiply-add
+            const __half2 r0 = __hfma2(f0, sAB, __hneg2(h0)), r1 = __hfma2(f1, sCD, __hneg2(h1));
+            mma_f16_16816(o[gi][i], ph, *reinterpret_cast<const uint32_t*>(&r0),
+                          *reinterpret_cast<const uint32_t*>(&r1));
+            mma_f16_16816(o[gi][i], pl, v0, v1);
+          }
           mma_f16_16816(o[gi][i], ph, v0, v1);
         }
       }
@@ -453,7 +483,7 @@ __global__ void __launch_bounds__(32 * MT * C, MINB) paged_decode_kernel(PdArgs 
       }
       if (pieces == 1) {
         const int tok = row / a.group;
-        pd_write8<float>(a, q.row0 + tok, kvh * a.group + row - tok * a.group, 8 * lane, x, l > 0.f ? 1.f / l : 0.f);
+        pd_write8<T>(a, q.row0 + tok, kvh * a.group + row - tok * a.group, 8 * lane, x, l > 0.f ? 1.f / l : 0.f);
       } else {
         Row8<float>::store(a.part_o + (slot_row + row) * kD + 8 * lane, x);
         if (lane == 0) a.part_ml[slot_row + row] = make_float2(top, l);

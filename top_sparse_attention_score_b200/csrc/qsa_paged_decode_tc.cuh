@@ -8,14 +8,15 @@
 // 16 rows and holds O in registers (8 warps an SM: 86 us for 2 x 131072 cells and one token,
 // 256 us for four).  Here sixteen warps do nothing else, the products cost no issue slots, and
 // their cost does not depend on the rows.  One CTA per SM:
-//   * sixteen warps fetch and convert: a lane loads 16 codes, makes them fp16(code * scale) and
-//     stores them into the K or V tile of 64 cells (128-byte swizzle; the same layout serves K as
-//     a K-major and V as an MN-major operand).  The loads of the next block are in flight in
-//     registers while this one converts, its cells' pages are looked up a block before that;
-//   * one thread issues S = Q K^T with Q in TMEM (so the products read each converted value from
-//     shared memory once), then O += P V with P in TMEM: 2 x 64 columns of S, 128 of Q, 256 of O;
+//   * sixteen warps fetch and convert, eight each of the even and the odd blocks: a lane loads 16
+//     codes at a time, makes them fp16(code * scale) and stores them into the K or V tile of 64
+//     cells (128-byte swizzle; the same layout serves K as a K-major and V as an MN-major
+//     operand).  Registers that a conversion empties are filled by the loads of the block after
+//     the next at once, so two blocks are in flight; pages are looked up a block before that;
+//   * one thread issues S = Q K^T with Q in TMEM (shared memory and L1 are one path of 128 bytes a
+//     cycle, and the converted tiles, written once and read once, already take 16 cycles a cell
+//     of it, the loads 8), then O += P V with P in TMEM: 2 x 64 columns of S, 128 of Q, 256 of O;
 //   * four warps own the rows: softmax with a lagging reference maximum, the end of each piece.
-// Products of a block: 512 + 512 cycles of the tensor pipe, 16 a cell of HBM's 23.
 //
 // q enters as fp16 (bf16 q of ordinary size is exact), K and V as fp16(code * scale), the weights as
 // fp16: roundings of 2^-12 each against an output rounded to 2^-12 or 2^-9.
@@ -105,8 +106,8 @@ __global__ void __launch_bounds__(kTdThreads, 1) paged_decode_tc_kernel(PdArgs a
   unsigned char* smem =
       reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(td_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   unsigned char* sk = smem;
-  unsigned char* sv = smem + kTdStages * kTdTile;
-  TdBarriers& tb = *reinterpret_cast<TdBarriers*>(smem + 2 * kTdStages * kTdTile);
+  unsigned char* sv = sk + kTdStages * kTdTile;
+  TdBarriers& tb = *reinterpret_cast<TdBarriers*>(sv + kTdStages * kTdTile);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int hkv = a.c.hkv;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -154,7 +155,7 @@ __global__ void __launch_bounds__(kTdThreads, 1) paged_decode_tc_kernel(PdArgs a
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kTdStages; ++i) {
-      mbar_init(&tb.k_full[i], kTdConvWarps / 2);
+      mbar_init(&tb.k_full[i], kTdConvWarps / 2);  // the eight warps of a parity
       mbar_init(&tb.v_full[i], kTdConvWarps / 2);
       mbar_init(&tb.k_empty[i], 1);
       mbar_init(&tb.v_empty[i], 1);
@@ -171,7 +172,7 @@ __global__ void __launch_bounds__(kTdThreads, 1) paged_decode_tc_kernel(PdArgs a
     tb.abort = 0u;
     mbar_init_fence();
   }
-  if (warp == 4) tmem_alloc(&tb.tmem_base, 512u);
+  if (warp == 5) tmem_alloc(&tb.tmem_base, 512u);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -181,16 +182,14 @@ __global__ void __launch_bounds__(kTdThreads, 1) paged_decode_tc_kernel(PdArgs a
 
   if (warp >= 8) {
     regs_shrink<kTdRegsConv>();
-    // ---------------- conversion: warps 0..7 of it K, 8..15 V; eight cells of each block
-    const int cw = warp - 8, part = cw & 7;
-    const bool is_v = cw >= 8;
+    // ---------------- conversion: eight cells of each block of this warp's parity, K and V
+    const int cw = warp - 8, part = cw & 7, st = cw >> 3;  // st: parity, and with it the stage
     const int sub = lane >> 2, j = lane & 3;  // cell 8 part + sub; 16-code chunk j of each 64 dims
     const int c = 8 * part + sub;
-    const int8_t* codes = is_v ? a.c.v : a.c.k;
-    const __half* scales = is_v ? a.c.vs : a.c.ks;
-    unsigned char* tiles = (is_v ? sv : sk) + c * 128;
-    uint64_t* full = is_v ? tb.v_full : tb.k_full;
-    uint64_t* empty = is_v ? tb.v_empty : tb.k_empty;
+    unsigned char* dst_k = sk + st * kTdTile + c * 128;
+    unsigned char* dst_v = sv + st * kTdTile + c * 128;
+    const int chunk0 = ((2 * j) ^ sub) << 4, chunk1 = ((2 * j + 1) ^ sub) << 4;
+    static_assert(kTdStages == 2, "a stage for each parity");
     // The lane's cell of the walk's block: page table entry and offset, kept up by addition.
     int entry = 0, off = 0;
     auto open_page = [&]() {
@@ -200,43 +199,45 @@ __global__ void __launch_bounds__(kTdThreads, 1) paged_decode_tc_kernel(PdArgs a
     };
     open_page();
     int at = 0;  // block of the walk
-    // row of the cell arrays of this lane's cell of the next block; -1: none
-    auto lookup = [&]() {
-      if (at >= nblocks) return static_cast<int64_t>(-1);
-      int page = -1;
-      if (walk.blk * kTdCells + c < walk.q.cells && entry < a.b.table_ld)
-        page = __ldg(a.b.table + static_cast<size_t>(walk.seq) * a.b.table_ld + entry);
-      const int64_t row = page < 0 || page >= a.b.pages
-                              ? static_cast<int64_t>(-1)
-                              : static_cast<int64_t>(page * a.b.page_cells + off) * hkv + walk.kvh;
-      if (++at < nblocks) {
-        if (td_next(a, walk)) {
-          open_page();
-        } else {
-          off += kTdCells;
-          while (off >= a.b.page_cells) off -= a.b.page_cells, ++entry;
-        }
+    auto advance = [&]() {
+      if (++at >= nblocks) return;
+      if (td_next(a, walk)) {
+        open_page();
+      } else {
+        off += kTdCells;
+        while (off >= a.b.page_cells) off -= a.b.page_cells, ++entry;
       }
-      return row;
+    };
+    // A block's page, as the table has it (nothing uses it before row_of: a use would wait for the
+    // load), with the lane's offset in it and the KV head.
+    struct Page {
+      int page, off, kvh;
+    };
+    auto lookup = [&]() {
+      Page g = {-1, off, walk.kvh};
+      if (at < nblocks && walk.blk * kTdCells + c < walk.q.cells && entry < a.b.table_ld)
+        g.page = __ldg(a.b.table + static_cast<size_t>(walk.seq) * a.b.table_ld + entry);
+      advance();
+      advance();
+      return g;
+    };
+    // row of the cell arrays; -1: no such cell
+    auto row_of = [&](const Page& g) {
+      return g.page < 0 || g.page >= a.b.pages ? -1 : (g.page * a.b.page_cells + g.off) * hkv + g.kvh;
     };
     struct Loaded {
       uint4 code[4];
       uint4 scale;
-      bool there;
     };
-    auto load = [&](Loaded& x, int64_t row) {
-      x.there = row >= 0;
-      const int8_t* src = codes + row * kD + 16 * j;
+    auto load = [&](Loaded& x, const int8_t* codes, const __half* scales, int row) {
+      const int8_t* src = codes + static_cast<size_t>(max(row, 0)) * kD + 16 * j;
 #pragma unroll
       for (int u = 0; u < 4; ++u)
-        x.code[u] = x.there ? __ldg(reinterpret_cast<const uint4*>(src + 64 * u)) : make_uint4(0u, 0u, 0u, 0u);
-      x.scale = x.there ? __ldg(reinterpret_cast<const uint4*>(scales + row * kNG)) : make_uint4(0u, 0u, 0u, 0u);
+        x.code[u] = row >= 0 ? __ldg(reinterpret_cast<const uint4*>(src + 64 * u)) : make_uint4(0u, 0u, 0u, 0u);
+      x.scale = row >= 0 ? __ldg(reinterpret_cast<const uint4*>(scales + static_cast<size_t>(row) * kNG))
+                         : make_uint4(0u, 0u, 0u, 0u);
     };
-    bool ok = true;
-    auto convert = [&](const Loaded& x, int i) {
-      const int st = i % kTdStages;
-      ok = ok && wait(empty + st, ((i / kTdStages) & 1) ^ 1);
-      unsigned char* dst = tiles + st * kTdTile;
+    auto convert = [&](const Loaded& x, unsigned char* dst) {
       const uint32_t sc[4] = {x.scale.x, x.scale.y, x.scale.z, x.scale.w};
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
@@ -244,78 +245,107 @@ __global__ void __launch_bounds__(kTdThreads, 1) paged_decode_tc_kernel(PdArgs a
         const __half2 pair = *reinterpret_cast<const __half2*>(&sc[u]);
         uint4 lo, hi;
         td_convert16(x.code[u], (j >> 1) ? __high2half2(pair) : __low2half2(pair), lo, hi);
-        *reinterpret_cast<uint4*>(dst + u * (kTdCells * 128) + (((2 * j) ^ sub) << 4)) = lo;
-        *reinterpret_cast<uint4*>(dst + u * (kTdCells * 128) + (((2 * j + 1) ^ sub) << 4)) = hi;
+        *reinterpret_cast<uint4*>(dst + u * (kTdCells * 128) + chunk0) = lo;
+        *reinterpret_cast<uint4*>(dst + u * (kTdCells * 128) + chunk1) = hi;
       }
-      if (!is_v) {
-        const bool cell_there = __shfl_sync(0xffffffffu, x.there, (lane & 7) << 2);  // of cell lane % 8
-        const uint32_t m = __ballot_sync(0xffffffffu, cell_there);
-        if (lane == 0) tb.valid[i & 3][part] = static_cast<uint8_t>(m);
-      }
+    };
+    bool ok = true;
+    if (st == 1) advance();
+    Loaded xk, xv;
+    Page page = lookup();
+    int row = row_of(page);
+    load(xk, a.c.k, a.c.ks, row);
+    load(xv, a.c.v, a.c.vs, row);
+    page = lookup();
+    for (int i = st; i < nblocks; i += 2) {
+      const uint32_t parity = ((i >> 1) & 1) ^ 1;
+      const int next = row_of(page);
+      ok = ok && wait(&tb.k_empty[st], parity);
+      convert(xk, dst_k);
+      load(xk, a.c.k, a.c.ks, next);
+      const bool there = __shfl_sync(0xffffffffu, row >= 0, (lane & 7) << 2);  // cell lane % 8 exists
+      const uint32_t m = __ballot_sync(0xffffffffu, there);
+      if (lane == 0) tb.valid[i & 3][part] = static_cast<uint8_t>(m);
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(full + st);
-    };
-    Loaded x[2];
-    int64_t row = lookup(), next = lookup();
-    load(x[0], row);
-    for (int i = 0; i < nblocks; i += 2) {
+      if (lane == 0) mbar_arrive(&tb.k_full[st]);
+      page = lookup();
+      ok = ok && wait(&tb.v_empty[st], parity);
+      convert(xv, dst_v);
+      load(xv, a.c.v, a.c.vs, next);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&tb.v_full[st]);
       row = next;
-      next = lookup();
-      load(x[1], row);
-      convert(x[0], i);
-      if (i + 1 >= nblocks) break;
-      row = next;
-      next = lookup();
-      load(x[0], row);
-      convert(x[1], i + 1);
     }
   } else if (warp >= 4) {
     regs_shrink<kTdRegsMma>();
-    if (warp == 4 && lane == 0) {
-      // ---------------- MMA: S of block i + 1 goes ahead of the product of block i
+    if (warp == 5) {
+      // ---------------- MMA: S of block i + 1 goes ahead of the product of block i.  The whole warp
+      // walks and waits, so descriptors stay in uniform registers; one lane issues.
       bool ok = true;
-      const uint32_t k0 = smem_u32(sk), v0 = smem_u32(sv);
-      auto wait1 = [&](uint64_t* bar, uint32_t parity) { return ok = fa_wait(bar, parity, &tb.abort, a.status); };
+      const bool lead = elect_one();
+      const uint64_t k0 = umma_desc_k_sw128(smem_u32(sk), 1024);
+      const uint64_t v0 = umma_desc_mn_sw128(smem_u32(sv), kTdCells * 128, 1024);
+      // blocks that are left of the pieces of the next scores and of the next product
       TdWalk ahead = walk;
+      int left_s = ahead.nb - ahead.blk, left_p = left_s;
+      auto advance = [&](TdWalk& w, int& left) {  // to the next block; true where it opens a piece
+        if (--left > 0) return false;
+        w.blk = w.nb - 1;
+        td_next(a, w);
+        left = w.nb;
+        return true;
+      };
       int pieces_q = 0, pieces_o = 0;  // pieces whose Q was awaited, whose O was begun
       auto scores = [&](int i) {
-        const bool opens = i == 0 || td_next(a, ahead);
-        if (opens && !wait1(&tb.q_ready, pieces_q++ & 1)) return;
-        const int st = i % kTdStages;
-        if (!wait1(&tb.k_full[st], (i / kTdStages) & 1)) return;
+        const bool opens = i == 0 || advance(ahead, left_s);
+        if (opens) ok = ok && wait(&tb.q_ready, pieces_q++ & 1);
+        const int st = i & 1;
+        ok = ok && wait(&tb.k_full[st], (i >> 1) & 1);
+        if (!ok) return;
         tc_fence_after();
-#pragma unroll 4
-        for (int ks = 0; ks < 16; ++ks)
-          umma_f16_ts(tmem + (i & 1) * kTdCells, tmem_q + ks * 8,
-                      umma_desc_k_sw128(k0 + st * kTdTile + (ks >> 2) * (kTdCells * 128) + (ks & 3) * 32, 1024),
-                      kIdescQK, ks > 0 ? 1u : 0u);
-        umma_commit(&tb.k_empty[st]);
-        umma_commit(&tb.s_full[i & 1]);
+        if (lead) {
+          const uint64_t kd = k0 + static_cast<uint32_t>(st * (kTdTile >> 4));
+          const uint32_t d = tmem + st * kTdCells;
+#pragma unroll
+          for (int ks = 0; ks < 16; ++ks)
+            umma_f16_ts(d, tmem_q + ks * 8, kd + (((ks >> 2) * (kTdCells * 128) + (ks & 3) * 32) >> 4), kIdescQK,
+                        ks > 0 ? 1u : 0u);
+          umma_commit(&tb.k_empty[st]);
+          umma_commit(&tb.s_full[st]);
+        }
+        __syncwarp();
       };
       scores(0);
       for (int i = 0; i < nblocks && ok; ++i) {
         if (i + 1 < nblocks) scores(i + 1);
         if (!ok) break;
-        const bool first = i == 0 || td_next(a, walk), last = i + 1 == nblocks || walk.blk + 1 == walk.nb;
+        const bool first = i == 0 || advance(walk, left_p), last = i + 1 == nblocks || left_p == 1;
         // the last piece's O must have been read out
-        if (first && pieces_o++ > 0 && !wait1(&tb.o_free, (pieces_o - 2) & 1)) break;
-        const int st = i % kTdStages;
-        if (!wait1(&tb.p_ready[i & 1], (i >> 1) & 1) || !wait1(&tb.v_full[st], (i / kTdStages) & 1)) break;
+        if (first && pieces_o++ > 0 && !(ok = wait(&tb.o_free, (pieces_o - 2) & 1))) break;
+        const int st = i & 1;
+        ok = wait(&tb.p_ready[st], (i >> 1) & 1) && wait(&tb.v_full[st], (i >> 1) & 1);
+        if (!ok) break;
         tc_fence_after();
+        if (lead) {
+          const uint64_t vd = v0 + static_cast<uint32_t>(st * (kTdTile >> 4));
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks)
-          umma_f16_ts(tmem_o, tmem + (i & 1) * kTdCells + ks * 8,
-                      umma_desc_mn_sw128(v0 + st * kTdTile + ks * 2048, kTdCells * 128, 1024), kIdescPV,
-                      first && ks == 0 ? 0u : 1u);
-        umma_commit(&tb.v_empty[st]);
-        umma_commit(&tb.pv_done);
-        if (last) umma_commit(&tb.o_full);
+          for (int ks = 0; ks < 4; ++ks)
+            umma_f16_ts(tmem_o, tmem + st * kTdCells + ks * 8, vd + (ks * 2048 >> 4), kIdescPV,
+                        first && ks == 0 ? 0u : 1u);
+          umma_commit(&tb.v_empty[st]);
+          umma_commit(&tb.pv_done);
+          if (last) umma_commit(&tb.o_full);
+        }
+        __syncwarp();
       }
-      umma_commit(&tb.drain);  // every MMA issued has completed once it fires
-      mbar_drain_wait(&tb.drain, 0);
+      if (lead) {  // every MMA issued has completed once it fires
+        umma_commit(&tb.drain);
+        mbar_drain_wait(&tb.drain, 0);
+      }
+      __syncwarp();
     }
-    __syncwarp();
   } else {
     regs_grow<kTdRegsSoftmax>();
     // ---------------- softmax and the ends of pieces: thread = row = TMEM lane
@@ -468,7 +498,7 @@ __global__ void __launch_bounds__(kTdThreads, 1) paged_decode_tc_kernel(PdArgs a
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 4) tmem_dealloc(tmem, 512u);
+  if (warp == 5) tmem_dealloc(tmem, 512u);
 }
 
 }  // namespace qsa
