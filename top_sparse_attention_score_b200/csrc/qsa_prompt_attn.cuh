@@ -578,85 +578,99 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFaThreads, 1)
       __syncwarp();
     } else if (warp == 9 && rank == 0) {
       // ---------------- MMA, for both CTAs.  The product O += P_j V_j of step j is issued after
-      // the scores of step j + 1, across query tiles too.
-      if (lane == 0) {
-        bool ok = true;
-        int n = 0;     // K and V tiles so far
-        int step = 0;  // key tiles whose scores were issued, over all query tiles
-        int q_tiles = 0;
-        const uint32_t q0 = smem_u32(sq), r0 = smem_u32(ring);
-        auto wait1 = [&](uint64_t* bar, uint32_t parity) { return ok = fa_wait(bar, parity, &fb.abort, a.status); };
-        auto take = [&](int at) {  // slot of the at-th K or V tile
-          wait1(&fb.full[at % kFaSlots], (at / kFaSlots) & 1);
-          tc_fence_after();
-          return at % kFaSlots;
-        };
-        auto scores = [&](int at) {  // S = Q K_step^T
-          const int b = step & 1, slot = take(at);
-          if (!ok) return;
+      // the scores of step j + 1, across query tiles too.  The whole warp waits and counts, so
+      // descriptors stay in uniform registers; one lane issues.
+      bool ok = true;
+      const bool lead = elect_one();
+      int n = 0;     // K and V tiles so far
+      int step = 0;  // key tiles whose scores were issued, over all query tiles
+      int q_tiles = 0;
+      const uint64_t q0 = umma_desc_k_sw128(smem_u32(sq), 1024), k0 = umma_desc_k_sw128(smem_u32(ring), 1024);
+      const uint64_t v0 = umma_desc_mn_sw128(smem_u32(ring), kFaN * 128, 1024);
+      auto wait1 = [&](uint64_t* bar, uint32_t parity) { return ok = ok && wait(bar, parity); };
+      auto commit = [&](uint64_t* bar) {
+        if (lead) umma2_commit(bar);
+        __syncwarp();
+      };
+      auto take = [&](int at) {  // slot of the at-th K or V tile
+        wait1(&fb.full[at % kFaSlots], (at / kFaSlots) & 1);
+        tc_fence_after();
+        return at % kFaSlots;
+      };
+      auto scores = [&](int at) {  // S = Q K_step^T
+        const int b = step & 1, slot = take(at);
+        if (!ok) return;
+        if (lead) {
+          const uint64_t kd = k0 + static_cast<uint32_t>(slot * (kFaSlotBytes >> 4));
+          const uint32_t d = tmem + b * kFaN;
 #pragma unroll
           for (int ks = 0; ks < 16; ++ks)
-            umma2_f16_ss(tmem + b * kFaN, umma_desc_k_sw128(q0 + (ks >> 2) * (kFaM * 128) + (ks & 3) * 32, 1024),
-                         umma_desc_k_sw128(r0 + slot * kFaSlotBytes + (ks >> 2) * (64 * 128) + (ks & 3) * 32, 1024),
-                         kIdescQK, ks > 0 ? 1u : 0u);
+            umma2_f16_ss(d, q0 + (((ks >> 2) * (kFaM * 128) + (ks & 3) * 32) >> 4),
+                         kd + (((ks >> 2) * (64 * 128) + (ks & 3) * 32) >> 4), kIdescQK, ks > 0 ? 1u : 0u);
           umma2_commit(&fb.empty[slot]);
           umma2_commit(&fb.s_full[b]);
-          ++step;
-        };
-        auto product = [&](int j, bool fresh, int at) {  // O (+)= P_j V_j
-          const int b = j & 1;
-          if (!wait1(&fb.p_ready[b], (j >> 1) & 1)) return;
-          const int slot = take(at);
-          if (!ok) return;
+        }
+        __syncwarp();
+        ++step;
+      };
+      auto product = [&](int j, bool fresh, int at) {  // O (+)= P_j V_j
+        const int b = j & 1;
+        if (!wait1(&fb.p_ready[b], (j >> 1) & 1)) return;
+        const int slot = take(at);
+        if (!ok) return;
+        if (lead) {
+          const uint64_t vd = v0 + static_cast<uint32_t>(slot * (kFaSlotBytes >> 4));
 #pragma unroll
           for (int ks = 0; ks < 8; ++ks)
-            umma2_f16_ts(tmem_o, tmem + b * kFaN + ks * 8,
-                         umma_desc_mn_sw128(r0 + slot * kFaSlotBytes + ks * 2048, kFaN * 128, 1024), kIdescPV,
-                         fresh && ks == 0 ? 0u : 1u);
+            umma2_f16_ts(tmem_o, tmem + b * kFaN + ks * 8, vd + (ks * 2048 >> 4), kIdescPV, fresh && ks == 0 ? 0u : 1u);
           umma2_commit(&fb.empty[slot]);
           umma2_commit(&fb.pv_done);
-        };
-        auto tile_steps = [&](int w) {  // key tiles of query tile w; -1: no more tiles
-          if (!wait1(&fb.tile_full[w & 1], (w >> 1) & 1)) return -1;
-          const int live = fb.tile[w & 1].live, keys = fb.tile[w & 1].keys;
-          mbar_arrive(&fb.tile_empty[w & 1]);
-          return live ? (keys + kFaN - 1) / kFaN : -1;
-        };
-        auto open_tile = [&](int at) {  // its Q and first scores
-          if (wait1(&fb.q_full, q_tiles++ & 1)) tc_fence_after(), scores(at);
-        };
-        int cur = tile_steps(0);
-        if (cur > 0) open_tile(n++);
-        for (int w = 0; ok && cur >= 0; ++w) {
-          // the last tile's O must have been read out before the first product overwrites it
-          bool fresh = true;
-          auto o_free = [&]() {
-            if (fresh && w > 0) wait1(&fb.o_free, (w - 1) & 1);
-            return ok;
-          };
-          for (int i = 0; i + 1 < cur && ok; ++i) {
-            scores(n++);
-            if (i + 2 == cur && ok) umma2_commit(&fb.q_empty);
-            if (ok && o_free()) product(step - 2, fresh, n++);
-            fresh = false;
-          }
-          if (!ok) break;
-          if (cur == 1) umma2_commit(&fb.q_empty);
-          const int next = tile_steps(w + 1);
-          if (!ok) break;
-          if (next > 0 && (cur == 0 || fa_test(&fb.q_full, q_tiles & 1))) {
-            // the next tile's Q is there: its first scores go ahead of this tile's last product
-            open_tile(n++);
-            if (ok && o_free() && cur > 0) product(step - 2, fresh, n++);
-          } else {
-            if (o_free() && cur > 0) product(step - 1, fresh, next > 0 ? n + 1 : n);
-            if (ok && next > 0) open_tile(n);
-            n += (cur > 0) + (next > 0);
-          }
-          if (ok) umma2_commit(&fb.o_full);
-          cur = next;
         }
-        // every MMA this thread issued has completed once `drain` fires
+        __syncwarp();
+      };
+      auto tile_steps = [&](int w) {  // key tiles of query tile w; -1: no more tiles
+        if (!wait1(&fb.tile_full[w & 1], (w >> 1) & 1)) return -1;
+        const int live = fb.tile[w & 1].live, keys = fb.tile[w & 1].keys;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&fb.tile_empty[w & 1]);
+        return live ? (keys + kFaN - 1) / kFaN : -1;
+      };
+      auto open_tile = [&](int at) {  // its Q and first scores
+        if (wait1(&fb.q_full, q_tiles++ & 1)) scores(at);
+      };
+      int cur = tile_steps(0);
+      if (cur > 0) open_tile(n++);
+      for (int w = 0; ok && cur >= 0; ++w) {
+        // the last tile's O must have been read out before the first product overwrites it
+        bool fresh = true;
+        auto o_free = [&]() {
+          if (fresh && w > 0) wait1(&fb.o_free, (w - 1) & 1);
+          return ok;
+        };
+        for (int i = 0; i + 1 < cur && ok; ++i) {
+          scores(n++);
+          if (i + 2 == cur && ok) commit(&fb.q_empty);
+          if (ok && o_free()) product(step - 2, fresh, n++);
+          fresh = false;
+        }
+        if (!ok) break;
+        if (cur == 1) commit(&fb.q_empty);
+        const int next = tile_steps(w + 1);
+        if (!ok) break;
+        const bool early = next > 0 && __any_sync(0xffffffffu, cur == 0 || fa_test(&fb.q_full, q_tiles & 1));
+        if (early) {
+          // the next tile's Q is there: its first scores go ahead of this tile's last product
+          open_tile(n++);
+          if (ok && o_free() && cur > 0) product(step - 2, fresh, n++);
+        } else {
+          if (o_free() && cur > 0) product(step - 1, fresh, next > 0 ? n + 1 : n);
+          if (ok && next > 0) open_tile(n);
+          n += (cur > 0) + (next > 0);
+        }
+        if (ok) commit(&fb.o_full);
+        cur = next;
+      }
+      if (lead) {  // every MMA issued has completed once `drain` fires
         umma2_commit(&fb.drain);
         mbar_drain_wait(&fb.drain, 0);
       }
