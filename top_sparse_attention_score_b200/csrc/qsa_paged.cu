@@ -108,9 +108,9 @@ struct DecodePlan {
 DecodePlan plan_decode(int nseq, int hkv, int group, int max_q, int64_t max_len, bool split, int sms) {
   DecodePlan p;
   p.mt = (max_q * group + 15) / 16;
-  p.groups = p.mt == 1 ? 4 : p.mt == 2 ? 2 : 1;
+  p.groups = p.mt == 1 ? 3 : 1;
   p.tc = !split && p.mt > 1;
-  p.ctas_per_sm = !p.tc && p.mt <= 3 ? 2 : 1;
+  p.ctas_per_sm = p.tc || p.mt > 3 ? 1 : p.mt == 2 ? 3 : 2;
   p.prows = 16 * p.mt;
   p.block_cells = p.tc ? qsa::kTdCells : 16 * p.groups;
   p.blocks = static_cast<int64_t>(nseq) * hkv * ((max_len + p.block_cells - 1) / p.block_cells);
@@ -155,7 +155,7 @@ cudaError_t launch_big(K kernel, std::atomic<uint64_t>& done, int grid, int thre
 template <typename T, int MT, int C, int STAGES, int MINB>
 cudaError_t launch_decode_mma(const qsa::PdArgs& a, int grid, cudaStream_t s) {
   static std::atomic<uint64_t> done{0};
-  return launch_big(qsa::paged_decode_kernel<T, MT, C, STAGES, MINB>, done, grid, 32 * MT * C,
+  return launch_big(qsa::paged_decode_kernel<T, MT, C, STAGES, MINB>, done, grid, 32 * qsa::kPdW * MT * C,
                     qsa::PdSmem<MT, C, STAGES, sizeof(T) == 4>::kBytes, a, s);
 }
 
@@ -169,11 +169,11 @@ template <typename T>
 int launch_decode(const qsa::PdArgs& a, const DecodePlan& p, int hq, cudaStream_t s) {
   cudaError_t e = cudaSuccess;
   if constexpr (sizeof(T) == 2) {
-    e = p.tc ? launch_decode_tc<T>(a, p.grid, s) : launch_decode_mma<T, 1, 4, 3, 2>(a, p.grid, s);
+    e = p.tc ? launch_decode_tc<T>(a, p.grid, s) : launch_decode_mma<T, 1, 3, 3, 2>(a, p.grid, s);
   } else {
     switch (p.mt) {
-      case 1: e = launch_decode_mma<T, 1, 4, 2, 2>(a, p.grid, s); break;
-      case 2: e = launch_decode_mma<T, 2, 2, 4, 2>(a, p.grid, s); break;
+      case 1: e = launch_decode_mma<T, 1, 3, 3, 2>(a, p.grid, s); break;
+      case 2: e = launch_decode_mma<T, 2, 1, 3, 3>(a, p.grid, s); break;
       case 3: e = launch_decode_mma<T, 3, 1, 5, 2>(a, p.grid, s); break;
       case 4: e = launch_decode_mma<T, 4, 1, 6, 1>(a, p.grid, s); break;
       case 5: e = launch_decode_mma<T, 5, 1, 8, 1>(a, p.grid, s); break;

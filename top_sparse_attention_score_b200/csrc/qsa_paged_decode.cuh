@@ -14,10 +14,13 @@
 //    the final rows itself.  Only the first and the last unit of a range can be partial, so CTA c
 //    has two partial slots: 2c for a unit begun before it, 2c + 1 for one that goes on after it.
 //    No counter or atomic orders anything.
-//  * MT warps hold the MT tiles of 16 query rows, C groups of MT warps take 16-cell blocks in
-//    turn.  A warp keeps 16 x 256 of O in registers (128 of them), so no score or weight is
-//    exchanged between warps; the C groups' results join once per piece through shared memory.
-//  * Cells arrive by cp.async in a ring of 16-cell stages a group owns (only its MT warps wait
+//  * Two warps hold a tile of 16 query rows, 128 dims each; a group of MT such pairs takes a
+//    16-cell block, C groups take blocks in turn and join once per piece through shared memory.
+//    A pair exchanges its partial scores (8 floats a lane) once a block and repeats the softmax.
+//    One warp with all 256 dims exchanges nothing, but its 128 registers of O leave 8 warps an SM
+//    and no room for independent instructions: 86 us for 2 x 131072 cells, 0.25 instructions a
+//    warp and cycle whatever their number.
+//  * Cells arrive by cp.async in a ring of 16-cell stages a group owns (only its warps wait
 //    for it).  Rows are 256 bytes without padding; 32-byte pairs of chunks are XOR-swizzled by
 //    the cell, so the fragment reads (8 bytes of 4 cells, 4 bytes of 4 cell pairs) hit all banks.
 //  * Codes become fp16 exactly (byte permute into 0x64xx, minus 1152) and feed mma.sync m16n8k16.
@@ -84,14 +87,22 @@ __device__ __forceinline__ PdSeq pd_seq(const PdArgs& a, int s) {
 // Cells that row j of the sequence sees (its last visible position + 1).
 __device__ __forceinline__ int pd_visible(const PdSeq& q, int j) { return q.len - q.n + 1 + j; }
 
-template <typename T>
-__device__ __forceinline__ float pd_to_float(T x);
-template <>
-__device__ __forceinline__ float pd_to_float(float x) { return x; }
-template <>
-__device__ __forceinline__ float pd_to_float(__half x) { return __half2float(x); }
-template <>
-__device__ __forceinline__ float pd_to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
+// Four consecutive values of a row.
+__device__ __forceinline__ void pd_load4(const float* p, float (&x)[4]) {
+  const float4 v = __ldg(reinterpret_cast<const float4*>(p));
+  x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+}
+__device__ __forceinline__ void pd_load4(const __half* p, float (&x)[4]) {
+  const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+  const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&v.x));
+  const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&v.y));
+  x[0] = a.x, x[1] = a.y, x[2] = b.x, x[3] = b.y;
+}
+__device__ __forceinline__ void pd_load4(const __nv_bfloat16* p, float (&x)[4]) {
+  const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+  x[0] = __uint_as_float(v.x << 16), x[1] = __uint_as_float(v.x & 0xffff0000u);
+  x[2] = __uint_as_float(v.y << 16), x[3] = __uint_as_float(v.y & 0xffff0000u);
+}
 
 // x = hi + lo with both in fp16 (lo holds the next 11 bits).
 __device__ __forceinline__ void pd_split2(float x, float y, uint32_t& hi, uint32_t& lo) {
@@ -121,34 +132,42 @@ __device__ __forceinline__ void pd_write8(const PdArgs& a, int row, int head, in
   Row8<T>::store(static_cast<T*>(a.out) + row * a.ldo + head * kD + d, x);
 }
 
+constexpr int kPdW = 2;           // warps of a row tile
+constexpr int kPdG = kNG / kPdW;  // scale groups of a warp
+
 template <int MT, int C, int STAGES, bool kSplit>
 struct PdSmem {
   static constexpr int kStageBytes = C * STAGES * static_cast<int>(sizeof(PdStage));
   static constexpr int kJoinBytes = C * MT * 16 * (kD + 4) * 4;  // rows padded to 260 floats
   static constexpr int kQBytes = MT * 16 * kD * 2 * (kSplit ? 2 : 1);
   static constexpr int kStatBytes = C * MT * 16 * 8;
-  static constexpr int kBytes = kQBytes + kStatBytes + (kStageBytes > kJoinBytes ? kStageBytes : kJoinBytes);
+  static constexpr int kExchBytes = C * MT * kPdW * 2 * 32 * 16;  // partial scores
+  // the join reuses the stages, Q and the exchange
+  static constexpr int kRing = kStageBytes + kQBytes + kExchBytes;
+  static constexpr int kBytes = kStatBytes + (kRing > kJoinBytes ? kRing : kJoinBytes);
 };
 
-// grid: CTAs that share the flat block list; block: 32 * MT * C.
+// grid: CTAs that share the flat block list; block: 64 * MT * C.
 template <typename T, int MT, int C, int STAGES, int MINB>
-__global__ void __launch_bounds__(32 * MT * C, MINB) paged_decode_kernel(PdArgs a) {
+__global__ void __launch_bounds__(32 * kPdW * MT * C, MINB) paged_decode_kernel(PdArgs a) {
   constexpr bool kSplit = sizeof(T) == 4;
-  constexpr int NT = 32 * MT * C, GT = 32 * MT;  // threads of the CTA, of a group
+  constexpr int GT = 32 * kPdW * MT, NT = GT * C;  // threads of a group, of the CTA
   constexpr int CB = 16 * C;                     // cells of a block of the flat list
   using Smem = PdSmem<MT, C, STAGES, kSplit>;
   extern __shared__ __align__(16) unsigned char smem_raw[];
-  uint4* sq = reinterpret_cast<uint4*>(smem_raw);  // [MT][hi, lo][16 k-steps][32 lanes]
-  float2* sstat = reinterpret_cast<float2*>(smem_raw + Smem::kQBytes);
-  PdStage* stages = reinterpret_cast<PdStage*>(smem_raw + Smem::kQBytes + Smem::kStatBytes);
-  float* sjoin = reinterpret_cast<float*>(stages);
+  PdStage* stages = reinterpret_cast<PdStage*>(smem_raw);
+  uint4* sq = reinterpret_cast<uint4*>(smem_raw + Smem::kStageBytes);  // [MT][hi, lo][16 k-steps][32 lanes]
+  float4* exch = reinterpret_cast<float4*>(smem_raw + Smem::kStageBytes + Smem::kQBytes);
+  float2* sstat = reinterpret_cast<float2*>(smem_raw + Smem::kBytes - Smem::kStatBytes);
+  float* sjoin = reinterpret_cast<float*>(smem_raw);
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int mt = warp % MT, cg = warp / MT;
+  const int dh = warp % kPdW, mt = warp / kPdW % MT, cg = warp / (kPdW * MT);  // dim half, row tile, group
   const int gtid = tid - cg * GT;
   const int g = lane >> 2, t = lane & 3;
   const int hkv = a.c.hkv;
   PdStage* ring = stages + cg * STAGES;
+  exch += (cg * MT + mt) * kPdW * 2 * 32 + lane;  // [half][n-tile][lane]
 
   griddep_wait();
 
@@ -247,9 +266,7 @@ __global__ void __launch_bounds__(32 * MT * C, MINB) paged_decode_kernel(PdArgs 
         float x[4] = {0.f, 0.f, 0.f, 0.f};
         if (r < nrow) {
           const int tok = r / a.group, head = kvh * a.group + r - tok * a.group;
-          const T* src = static_cast<const T*>(a.q) + (q.row0 + tok) * a.ldq + head * kD + d0;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) x[i] = pd_to_float(src[i]);
+          pd_load4(static_cast<const T*>(a.q) + (q.row0 + tok) * a.ldq + head * kD + d0, x);
         }
         if constexpr (kSplit) {
           pd_split2(x[0], x[1], hi[h], lo[h]);
@@ -271,22 +288,21 @@ __global__ void __launch_bounds__(32 * MT * C, MINB) paged_decode_kernel(PdArgs 
     __syncthreads();
 
     float m_run[2] = {kAttnNoMax, kAttnNoMax}, l_run[2] = {0.f, 0.f};
-    float o[kNG][4][4];
+    float o[kPdG][4][4];
 #pragma unroll
-    for (int gi = 0; gi < kNG; ++gi)
+    for (int gi = 0; gi < kPdG; ++gi)
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int c = 0; c < 4; ++c) o[gi][i][c] = 0.f;
-    const uint4* mq = sq + mt * (kSplit ? 2 : 1) * 16 * 32 + lane;
+    const uint4* mq = sq + (mt * (kSplit ? 2 : 1) * 16 + 2 * kPdG * dh) * 32 + lane;
 
     int slot = 0;
     for (int blk = blk0; blk < blk1; ++blk) {
       // block blk has landed for this thread; after the barrier for the group, and every
       // warp of it has left block blk - 1, whose stage the fetch below refills
       cp_async_wait<STAGES - 2>();
-      if constexpr (MT == 1) __syncwarp();
-      else asm volatile("bar.sync %0, %1;\n" ::"r"(1 + cg), "n"(GT) : "memory");
+      asm volatile("bar.sync %0, %1;\n" ::"r"(1 + cg), "n"(GT) : "memory");
       const int next = lookup(blk + STAGES);
       if (blk + STAGES - 1 < blk1) fetch(ring[slot == 0 ? STAGES - 1 : slot - 1], look[STAGES - 1]);
       cp_async_commit();
@@ -305,13 +321,13 @@ __global__ void __launch_bounds__(32 * MT * C, MINB) paged_decode_kernel(PdArgs 
       for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
         for (int c = 0; c < 4; ++c) s[nt][c] = 0.f;
-      uint4 ksw[2][2];  // the 8 scales of cells 8 nt + 2t and 8 nt + 2t + 1
+      uint2 ksw[2][2];  // this half's scales of cells 8 nt + 2t and 8 nt + 2t + 1
 #pragma unroll
       for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
-        for (int c = 0; c < 2; ++c) ksw[nt][c] = *reinterpret_cast<const uint4*>(st.ks + (8 * nt + 2 * t + c) * kNG);
+        for (int c = 0; c < 2; ++c) ksw[nt][c] = *reinterpret_cast<const uint2*>(st.ks + (8 * nt + 2 * t + c) * kNG + kPdG * dh);
 #pragma unroll
-      for (int qg = 0; qg < kNG; ++qg) {
+      for (int qg = 0; qg < kPdG; ++qg) {
         const uint4 qa = mq[(2 * qg) * 32], qb = mq[(2 * qg + 1) * 32];
         const uint32_t a0[4] = {qa.x, qa.y, qa.z, qa.w}, a1[4] = {qb.x, qb.y, qb.z, qb.w};
         uint32_t c0[4], c1[4];
@@ -322,7 +338,7 @@ __global__ void __launch_bounds__(32 * MT * C, MINB) paged_decode_kernel(PdArgs 
         }
 #pragma unroll
         for (int nt = 0; nt < 2; ++nt) {
-          const uint2 kw = *reinterpret_cast<const uint2*>(st.k + pd_koff(8 * nt + g, 32 * qg + 8 * t));
+          const uint2 kw = *reinterpret_cast<const uint2*>(st.k + pd_koff(8 * nt + g, 128 * dh + 32 * qg + 8 * t));
           const uint32_t x0 = kw.x ^ 0x80808080u, x1 = kw.y ^ 0x80808080u;
           const uint32_t b00 = i8x2_to_h2(x0, 0x4140u), b01 = i8x2_to_h2(x0, 0x4342u);
           const uint32_t b10 = i8x2_to_h2(x1, 0x4140u), b11 = i8x2_to_h2(x1, 0x4342u);
@@ -342,6 +358,15 @@ __global__ void __launch_bounds__(32 * MT * C, MINB) paged_decode_kernel(PdArgs 
           s[nt][2] = fmaf(sa, acc[2], s[nt][2]);
           s[nt][3] = fmaf(sb, acc[3], s[nt][3]);
         }
+      }
+      // ---- the pair's partial scores add up (the same sum in both warps)
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt) exch[(dh * 2 + nt) * 32] = make_float4(s[nt][0], s[nt][1], s[nt][2], s[nt][3]);
+      asm volatile("bar.sync %0, %1;\n" ::"r"(1 + C + cg * MT + mt), "n"(32 * kPdW) : "memory");
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt) {
+        const float4 y = exch[((dh ^ 1) * 2 + nt) * 32];
+        s[nt][0] += y.x, s[nt][1] += y.y, s[nt][2] += y.z, s[nt][3] += y.w;
       }
       // ---- masks, running maximum, weights
       float mx[2] = {-INFINITY, -INFINITY};
@@ -373,7 +398,7 @@ __global__ void __launch_bounds__(32 * MT * C, MINB) paged_decode_kernel(PdArgs 
           l_run[r] *= alpha;
           m_run[r] = mnew;
 #pragma unroll
-          for (int gi = 0; gi < kNG; ++gi)
+          for (int gi = 0; gi < kPdG; ++gi)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               o[gi][i][2 * r] *= alpha;
@@ -402,13 +427,13 @@ __global__ void __launch_bounds__(32 * MT * C, MINB) paged_decode_kernel(PdArgs 
         ph[2] = pack_half2(s[1][0], s[1][1]);
         ph[3] = pack_half2(s[1][2], s[1][3]);
       }
-      uint4 vsw[4];  // the scales of cells 2t, 2t+1, 2t+8, 2t+9
+      uint2 vsw[4];  // this half's scales of cells 2t, 2t+1, 2t+8, 2t+9
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        vsw[j] = *reinterpret_cast<const uint4*>(st.vs + (2 * t + (j & 1) + 8 * (j >> 1)) * kNG);
+        vsw[j] = *reinterpret_cast<const uint2*>(st.vs + (2 * t + (j & 1) + 8 * (j >> 1)) * kNG + kPdG * dh);
 #pragma unroll
-      for (int gi = 0; gi < kNG; ++gi) {
-        const int d = 32 * gi + 4 * g;  // column g of n-tile i is dim 32 gi + 4 g + i
+      for (int gi = 0; gi < kPdG; ++gi) {
+        const int d = 128 * dh + 32 * gi + 4 * g;  // column g of n-tile i is dim 32 gi + 4 g + i of the half
         const uint32_t wA = *reinterpret_cast<const uint32_t*>(st.v + pd_voff(2 * t, d)) ^ 0x80808080u;
         const uint32_t wB = *reinterpret_cast<const uint32_t*>(st.v + pd_voff(2 * t + 1, d)) ^ 0x80808080u;
         const uint32_t wC = *reinterpret_cast<const uint32_t*>(st.v + pd_voff(2 * t + 8, d)) ^ 0x80808080u;
@@ -445,17 +470,17 @@ __global__ void __launch_bounds__(32 * MT * C, MINB) paged_decode_kernel(PdArgs 
       l_run[r] += __shfl_xor_sync(0xffffffffu, l_run[r], 2);
     }
 
-    // ---- the C groups join in shared memory (the stages are free: every copy has landed)
+    // ---- the C groups join in shared memory (stages and Q are free: every copy has landed)
     __syncthreads();
     constexpr int kRow = kD + 4;  // floats of a joined row
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       const int row = (cg * MT + mt) * 16 + g + 8 * r;
-      if (t == 0) sstat[row] = make_float2(l_run[r] > 0.f ? m_run[r] : -INFINITY, l_run[r]);
+      if (t == 0 && dh == 0) sstat[row] = make_float2(l_run[r] > 0.f ? m_run[r] : -INFINITY, l_run[r]);
 #pragma unroll
-      for (int gi = 0; gi < kNG; ++gi) {
+      for (int gi = 0; gi < kPdG; ++gi) {
         // C element (row, col 2t) of n-tile i, group gi is dim 32 gi + 8 t + i; col 2t+1 is +4
-        float* dst = sjoin + row * kRow + 32 * gi + 8 * t;
+        float* dst = sjoin + row * kRow + 128 * dh + 32 * gi + 8 * t;
         *reinterpret_cast<float4*>(dst) =
             make_float4(o[gi][0][2 * r], o[gi][1][2 * r], o[gi][2][2 * r], o[gi][3][2 * r]);
         *reinterpret_cast<float4*>(dst + 4) =
@@ -464,7 +489,7 @@ __global__ void __launch_bounds__(32 * MT * C, MINB) paged_decode_kernel(PdArgs 
     }
     __syncthreads();
     const size_t slot_row = (2 * static_cast<size_t>(blockIdx.x) + (blk0 == 0 ? 1 : 0)) * a.prows;
-    for (int row = warp; row < nrow; row += MT * C) {
+    for (int row = warp; row < nrow; row += kPdW * MT * C) {
       float2 st[C];
       float top = -INFINITY, l = 0.f, x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
