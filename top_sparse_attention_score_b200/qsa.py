@@ -9,6 +9,7 @@ no fallback: if the library is missing, ``load()`` raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 
@@ -360,15 +361,15 @@ def _packed(t, heads, dtype, device, name):
     """(pointer, row stride) of packed rows [rows][heads][256] whose heads are contiguous."""
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, the call on {device}")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    n, h, d = t.shape
+    shape = t.shape
+    if len(shape) != 3 or shape[1] != heads or shape[2] != D:
+        raise ValueError(f"{name} must be [rows][{heads}][{D}], got {tuple(shape)}")
     ld, sh, sd = t.stride()
-    if h != heads or d != D:
-        raise ValueError(f"{name} must be [rows][{heads}][{D}], got {tuple(t.shape)}")
-    if sd != 1 or (h > 1 and sh != D):
+    if sd != 1 or (sh != D and heads > 1):
         raise ValueError(f"{name}: a row's {heads} x {D} values must be contiguous, strides {t.stride()}")
-    return t.data_ptr(), ld if n > 1 else heads * D
+    return t.data_ptr(), ld if shape[0] > 1 else heads * D
 
 
 def _same_rows(t, rows, name):
@@ -376,19 +377,29 @@ def _same_rows(t, rows, name):
         raise ValueError(f"{name} has {t.shape[0]} rows, the call has {rows}")
 
 
+_get_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_stream_of = _raw_stream or (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _here(device, stream):
+    """Whether a call needs no change of torch's current device and stream: its tensors are on
+    the current device and no stream is given."""
+    return stream is None and device.index == _get_device()
+
+
 class _On:
     """The device of a call's tensors as the current one, and `stream` as torch's current
-    stream there (for what the call allocates); a no-op where both are already so."""
-    __slots__ = ("dev", "stream", "held")
+    stream there (for what the call allocates)."""
+    __slots__ = ("held",)
 
     def __init__(self, device, stream):
-        self.dev, self.stream, self.held = device, stream, ()
+        self.held = [torch.cuda.device(device)]
+        if stream is not None:
+            if stream.device != device:
+                raise ValueError(f"the stream is on {stream.device}, the call on {device}")
+            self.held.append(torch.cuda.stream(stream))
 
     def __enter__(self):
-        if self.dev.index != torch.cuda.current_device():
-            self.held = (torch.cuda.device(self.dev),)
-        if self.stream is not None:
-            self.held += (torch.cuda.stream(self.stream),)
         for c in self.held:
             c.__enter__()
 
@@ -413,69 +424,88 @@ def _batch_on(cache, batch):
 def paged_write(cache: PagedCache, batch: Batch, k, v, stream=None) -> None:
     """Quantise packed rows k, v [rows][hkv][256] (float32, float16 or bfloat16; row strides
     free) into the cells of the batch's positions."""
+    dev = cache.device
+    if not _here(dev, stream):
+        with _On(dev, stream):
+            return paged_write(cache, batch, k, v)
     _batch_on(cache, batch)
-    code = _dtype_code(k.dtype)
+    dtype = k.dtype
+    code = _dtype_code(dtype)
     rows = k.shape[0]
-    kp, ldk = _packed(k, cache.hkv, k.dtype, cache.device, "k")
-    vp, ldv = _packed(v, cache.hkv, k.dtype, cache.device, "v")
+    kp, ldk = _packed(k, cache.hkv, dtype, dev, "k")
+    vp, ldv = _packed(v, cache.hkv, dtype, dev, "v")
     _same_rows(v, rows, "v")
-    with _On(cache.device, None):
-        _check(load().qsa_paged_write(cache._ref, batch._ref, rows, code, kp, ldk, vp, ldv, _stream(stream)))
+    _check(load().qsa_paged_write(cache._ref, batch._ref, rows, code, kp, ldk, vp, ldv, _stream_of(dev.index)))
 
 
 def paged_read(cache: PagedCache, batch: Batch, rows: int, dtype=torch.float16, k=None, v=None, stream=None):
     """(k, v) [rows][hkv][256]: the batch's cells as values, rounded once to dtype.  Rows of
     no sequence are left as they were (undefined in arrays that this call allocates)."""
+    dev = cache.device
+    if not _here(dev, stream):
+        with _On(dev, stream):
+            return paged_read(cache, batch, rows, dtype, k, v)
     _batch_on(cache, batch)
     code = _dtype_code(dtype)
-    with _On(cache.device, stream):
-        if k is None:
-            k = torch.empty(rows, cache.hkv, D, dtype=dtype, device=cache.device)
-        if v is None:
-            v = torch.empty(rows, cache.hkv, D, dtype=dtype, device=cache.device)
-        kp, ldk = _packed(k, cache.hkv, dtype, cache.device, "k")
-        vp, ldv = _packed(v, cache.hkv, dtype, cache.device, "v")
-        _same_rows(k, rows, "k")
-        _same_rows(v, rows, "v")
-        _check(load().qsa_paged_read(cache._ref, batch._ref, rows, code, kp, ldk, vp, ldv, _stream(stream)))
+    hkv = cache.hkv
+    if k is None:
+        k = torch.empty((rows, hkv, D), dtype=dtype, device=dev)
+    if v is None:
+        v = torch.empty((rows, hkv, D), dtype=dtype, device=dev)
+    kp, ldk = _packed(k, hkv, dtype, dev, "k")
+    vp, ldv = _packed(v, hkv, dtype, dev, "v")
+    _same_rows(k, rows, "k")
+    _same_rows(v, rows, "v")
+    _check(load().qsa_paged_read(cache._ref, batch._ref, rows, code, kp, ldk, vp, ldv, _stream_of(dev.index)))
     return k, v
 
 
+@functools.lru_cache(maxsize=256)
 def paged_decode_workspace_bytes(nseq: int, hq: int, hkv: int, max_q: int, max_len: int) -> int:
     return int(load().qsa_paged_decode_workspace_bytes(nseq, hq, hkv, max_q, max_len))
+
+
+def _check_ws(ws, dev):
+    if ws.device != dev or not ws.is_contiguous():
+        raise ValueError(f"ws must be contiguous on {dev}")
 
 
 def paged_decode(cache: PagedCache, batch: Batch, q, scale: float = 1 / 16, max_q: int = 1, max_len=None, gate=None,
                  out=None, ws=None, stream=None):
     """Attention of each sequence's newest rows (at most max_q) over all its cells, at most
     max_len (default: what the table can hold).  q, gate, out: [rows][hq][256] of one type.
-    Rows of no sequence are left as they were (undefined in an output allocated here)."""
+    Rows of no sequence are left as they were (undefined in an output allocated here).  A
+    workspace passed as ws serves one call at a time; without one the call allocates it."""
+    dev = cache.device
+    if not _here(dev, stream):
+        with _On(dev, stream):
+            return paged_decode(cache, batch, q, scale, max_q, max_len, gate, out, ws)
     _batch_on(cache, batch)
-    code = _dtype_code(q.dtype)
+    dtype = q.dtype
+    code = _dtype_code(dtype)
     rows, hq = q.shape[0], q.shape[1]
-    dev, dtype = cache.device, q.dtype
     if max_len is None:
         max_len = min(batch.width * cache.page_cells, (1 << 31) - 1)
     qp, ldq = _packed(q, hq, dtype, dev, "q")
-    gp, ldg = (None, 0) if gate is None else _packed(gate, hq, dtype, dev, "gate")
+    gp, ldg = None, 0
     if gate is not None:
+        gp, ldg = _packed(gate, hq, dtype, dev, "gate")
         _same_rows(gate, rows, "gate")
-    lib = load()
-    with _On(dev, stream):
-        if out is None:
-            out = torch.empty(rows, hq, D, dtype=dtype, device=dev)
-        op, ldo = _packed(out, hq, dtype, dev, "out")
-        _same_rows(out, rows, "out")
-        if ws is None:
-            need = lib.qsa_paged_decode_workspace_bytes(batch.nseq, hq, cache.hkv, max_q, max_len)
-            ws = torch.empty(need or 16, dtype=torch.uint8, device=dev)
-        elif ws.device != dev or not ws.is_contiguous():
-            raise ValueError(f"ws must be contiguous on {dev}")
-        _check(lib.qsa_paged_decode(cache._ref, batch._ref, rows, max_q, max_len, code, hq, qp, ldq, gp, ldg, scale,
-                                    ws.data_ptr(), ws.numel() * ws.element_size(), op, ldo, _stream(stream)))
+    if out is None:
+        out = torch.empty((rows, hq, D), dtype=dtype, device=dev)
+    op, ldo = _packed(out, hq, dtype, dev, "out")
+    _same_rows(out, rows, "out")
+    if ws is None:
+        need = paged_decode_workspace_bytes(batch.nseq, hq, cache.hkv, max_q, max_len)
+        ws = torch.empty(need or 16, dtype=torch.uint8, device=dev)
+    else:
+        _check_ws(ws, dev)
+    _check(load().qsa_paged_decode(cache._ref, batch._ref, rows, max_q, max_len, code, hq, qp, ldq, gp, ldg, scale,
+                                   ws.data_ptr(), ws.nbytes, op, ldo, _stream_of(dev.index)))
     return out
 
 
+@functools.lru_cache(maxsize=256)
 def prompt_attn_workspace_bytes(nseq: int, rows_q: int, rows_k: int, hq: int, hkv: int) -> int:
     return int(load().qsa_prompt_attn_workspace_bytes(nseq, rows_q, rows_k, hq, hkv))
 
@@ -483,39 +513,46 @@ def prompt_attn_workspace_bytes(nseq: int, rows_q: int, rows_k: int, hq: int, hk
 def prompt_attn(q, k, v, cu_q, cu_k=None, scale: float = 1 / 16, gate=None, out=None, ws=None, stream=None):
     """Causal attention over packed prompts: q, gate, out [rows][hq][256], k, v [keys][hkv][256]
     (float16 or bfloat16, row strides free), cu_q / cu_k int32 [nseq + 1] (cu_k None: cu_q).
-    Rows of no sequence are left as they were (undefined in an output allocated here)."""
+    Rows of no sequence are left as they were (undefined in an output allocated here).  A
+    workspace passed as ws serves one call at a time; without one the call allocates it."""
+    dev, dtype = q.device, q.dtype
+    if dev.type != "cuda":
+        raise ValueError("q must be a CUDA tensor")
+    if not _here(dev, stream):
+        with _On(dev, stream):
+            return prompt_attn(q, k, v, cu_q, cu_k, scale, gate, out, ws)
     if cu_k is None:
         cu_k = cu_q
-    _dev(cu_q, torch.int32, "cu_q")
-    _dev(cu_k, torch.int32, "cu_k")
-    if cu_q.dim() != 1 or cu_q.shape != cu_k.shape or cu_q.shape[0] < 2:
-        raise ValueError(f"cu_q and cu_k must be [nseq + 1], got {tuple(cu_q.shape)}, {tuple(cu_k.shape)}")
-    dev, dtype = q.device, q.dtype
-    if cu_q.device != dev or cu_k.device != dev:
-        raise ValueError(f"cu_q and cu_k must be on {dev}")
+    for t, name in ((cu_q, "cu_q"), (cu_k, "cu_k")):
+        _dev(t, torch.int32, name)
+        if t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, q on {dev}")
+        if t.dim() != 1 or t.shape != cu_q.shape or t.shape[0] < 2:
+            raise ValueError(f"cu_q and cu_k must be [nseq + 1], got {tuple(cu_q.shape)}, {tuple(cu_k.shape)}")
     code = _dtype_code(dtype)
-    rows, hq, hkv = q.shape[0], q.shape[1], k.shape[1]
+    rows, hq, keys, hkv = q.shape[0], q.shape[1], k.shape[0], k.shape[1]
     qp, ldq = _packed(q, hq, dtype, dev, "q")
     kp, ldk = _packed(k, hkv, dtype, dev, "k")
     vp, ldv = _packed(v, hkv, dtype, dev, "v")
-    _same_rows(v, k.shape[0], "v")
-    gp, ldg = (None, 0) if gate is None else _packed(gate, hq, dtype, dev, "gate")
+    _same_rows(v, keys, "v")
+    gp, ldg = None, 0
     if gate is not None:
+        gp, ldg = _packed(gate, hq, dtype, dev, "gate")
         _same_rows(gate, rows, "gate")
-    with _On(dev, stream):
-        if out is None:
-            out = torch.empty(rows, hq, D, dtype=dtype, device=dev)
-        op, ldo = _packed(out, hq, dtype, dev, "out")
-        _same_rows(out, rows, "out")
-        lib, nseq, keys = load(), cu_q.shape[0] - 1, k.shape[0]
-        if ws is None:
-            need = lib.qsa_prompt_attn_workspace_bytes(nseq, rows, keys, hq, hkv)
-            ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-        elif ws.device != dev or not ws.is_contiguous():
-            raise ValueError(f"ws must be contiguous on {dev}")
-        _check(lib.qsa_prompt_attn(nseq, cu_q.data_ptr(), cu_k.data_ptr(), rows, keys, code, hq, hkv, qp, ldq, kp, ldk,
-                                   vp, ldv, gp, ldg, scale, _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(),
-                                   op, ldo, _stream(stream)))
+    if out is None:
+        out = torch.empty((rows, hq, D), dtype=dtype, device=dev)
+    op, ldo = _packed(out, hq, dtype, dev, "out")
+    _same_rows(out, rows, "out")
+    nseq = cu_q.shape[0] - 1
+    if ws is None:
+        need = prompt_attn_workspace_bytes(nseq, rows, keys, hq, hkv)
+        if need:
+            ws = torch.empty(need, dtype=torch.uint8, device=dev)
+    else:
+        _check_ws(ws, dev)
+    _check(load().qsa_prompt_attn(nseq, cu_q.data_ptr(), cu_k.data_ptr(), rows, keys, code, hq, hkv, qp, ldq, kp, ldk, vp,
+                                  ldv, gp, ldg, scale, _ptr(ws), 0 if ws is None else ws.nbytes, op, ldo,
+                                  _stream_of(dev.index)))
     return out
 
 
