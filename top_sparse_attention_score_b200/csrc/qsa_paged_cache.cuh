@@ -145,6 +145,34 @@ struct Row8<__nv_bfloat16> {
   }
 };
 
+// x *= sigmoid(gate), elementwise.  fp32 rows by the exact function; 16-bit rows, which are rounded
+// at once, by the hardware's 2^x and one reciprocal for two values (a, b): 1 / a = b / (a b).  With
+// a = 1 + 2^(-g log2 e) cut at 2^60 (sigmoid at 2^-60) the product stays finite; 2^-21 relative.
+__device__ __forceinline__ void gate_row8(const Row8<float>& g, float (&x)[8]) {
+  float v[8];
+  g.get(v);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) x[e] *= gate_factor(v[e]);
+}
+template <typename T>
+__device__ __forceinline__ void gate_row8(const Row8<T>& g, float (&x)[8]) {
+  float v[8];
+  g.get(v);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(v[e] * -1.4426950408889634f));
+    v[e] = fminf(1.f + y, 1.152921504606847e18f);
+  }
+#pragma unroll
+  for (int e = 0; e < 8; e += 2) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v[e] * v[e + 1]));
+    x[e] *= r * v[e + 1];
+    x[e + 1] *= r * v[e];
+  }
+}
+
 constexpr int kPagedWarps = 4;  // packed rows per CTA of the write and the read
 
 // Head row i of a packed row's 2 * hkv: K of head i for i < hkv, else V of head i - hkv.

@@ -116,19 +116,21 @@ __device__ __forceinline__ void pd_split2(float x, float y, uint32_t& hi, uint32
 __device__ __forceinline__ int pd_koff(int c, int d) { return c * kD + (d ^ ((c & 7) << 5)); }
 __device__ __forceinline__ int pd_voff(int c, int d) { return c * kD + (d ^ (((c >> 1) & 7) << 5)); }
 
-// One row of 8 output values: o * inv, gated, in T.
+// The gate of 8 output values, to be loaded early.
 template <typename T>
-__device__ __forceinline__ void pd_write8(const PdArgs& a, int row, int head, int d, float (&x)[8], float inv) {
+__device__ __forceinline__ Row8<T> pd_gate8(const PdArgs& a, int row, int head, int d) {
+  Row8<T> g;
+  if (a.gate) g.load(static_cast<const T*>(a.gate) + row * a.ldg + head * kD + d);
+  return g;
+}
+
+// 8 output values of a row: o * inv, gated, in T.
+template <typename T>
+__device__ __forceinline__ void pd_write8(const PdArgs& a, int row, int head, int d, float (&x)[8], float inv,
+                                          const Row8<T>& gate) {
 #pragma unroll
   for (int e = 0; e < 8; ++e) x[e] *= inv;
-  if (a.gate) {
-    Row8<T> graw;
-    graw.load(static_cast<const T*>(a.gate) + row * a.ldg + head * kD + d);
-    float g[8];
-    graw.get(g);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] *= gate_factor(g[e]);
-  }
+  if (a.gate) gate_row8(gate, x);
   Row8<T>::store(static_cast<T*>(a.out) + row * a.ldo + head * kD + d, x);
 }
 
@@ -490,6 +492,9 @@ __global__ void __launch_bounds__(32 * kPdW * MT * C, MINB) paged_decode_kernel(
     __syncthreads();
     const size_t slot_row = (2 * static_cast<size_t>(blockIdx.x) + (blk0 == 0 ? 1 : 0)) * a.prows;
     for (int row = warp; row < nrow; row += kPdW * MT * C) {
+      const int tok = row / a.group, head = kvh * a.group + row - tok * a.group;
+      Row8<T> gate;
+      if (pieces == 1) gate = pd_gate8<T>(a, q.row0 + tok, head, 8 * lane);
       float2 st[C];
       float top = -INFINITY, l = 0.f, x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -507,8 +512,7 @@ __global__ void __launch_bounds__(32 * kPdW * MT * C, MINB) paged_decode_kernel(
         x[4] = fmaf(w, hi.x, x[4]), x[5] = fmaf(w, hi.y, x[5]), x[6] = fmaf(w, hi.z, x[6]), x[7] = fmaf(w, hi.w, x[7]);
       }
       if (pieces == 1) {
-        const int tok = row / a.group;
-        pd_write8<T>(a, q.row0 + tok, kvh * a.group + row - tok * a.group, 8 * lane, x, l > 0.f ? 1.f / l : 0.f);
+        pd_write8<T>(a, q.row0 + tok, head, 8 * lane, x, l > 0.f ? 1.f / l : 0.f, gate);
       } else {
         Row8<float>::store(a.part_o + (slot_row + row) * kD + 8 * lane, x);
         if (lane == 0) a.part_ml[slot_row + row] = make_float2(top, l);
@@ -536,13 +540,15 @@ __global__ void __launch_bounds__(32 * kPjWarps) paged_join_kernel(PdArgs a) {
   if (tok >= a.max_q) return;
   float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   if (q.cells == 0) {
-    if (warp == 0) pd_write8<T>(a, row, head, 8 * lane, x, 0.f);
+    if (warp == 0) pd_write8<T>(a, row, head, 8 * lane, x, 0.f, pd_gate8<T>(a, row, head, 8 * lane));
     return;
   }
   const int kvh = head / a.group, unit = s * a.c.hkv + kvh;
   const int2 info = __ldcg(a.unit + unit);
   if (info.y == 1) return;  // written by its CTA
   const size_t in_slot = static_cast<size_t>(tok) * a.group + head - kvh * a.group;
+  Row8<T> gate;
+  if (warp == 0) gate = pd_gate8<T>(a, row, head, 8 * lane);
   // each warp its pieces, online
   float top = -INFINITY, l = 0.f;
   for (int j0 = warp; j0 < info.y; j0 += 4 * kPjWarps) {
@@ -596,7 +602,7 @@ __global__ void __launch_bounds__(32 * kPjWarps) paged_join_kernel(PdArgs a) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) x[i] = fmaf(e, so[w][8 * lane + i], x[i]);
   }
-  pd_write8<T>(a, row, head, 8 * lane, x, total > 0.f ? 1.f / total : 0.f);
+  pd_write8<T>(a, row, head, 8 * lane, x, total > 0.f ? 1.f / total : 0.f, gate);
 }
 
 }  // namespace qsa

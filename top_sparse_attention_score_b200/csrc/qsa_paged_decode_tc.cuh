@@ -474,6 +474,11 @@ __global__ void __launch_bounds__(kTdThreads, 1) paged_decode_tc_kernel(PdArgs a
 #pragma unroll 1
         for (int c = 0; c < kD; c += 32) {
           uint32_t o[32];
+          Row8<T> gate[4];
+          if (r < nrow && pieces == 1) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) gate[u] = pd_gate8<T>(a, q.row0 + tok, head, c + 8 * u);
+          }
           tmem_ld32(tmem_o + lanes + c, o);
           tmem_ld_wait();
           if (r < nrow && ok) {
@@ -482,7 +487,7 @@ __global__ void __launch_bounds__(kTdThreads, 1) paged_decode_tc_kernel(PdArgs a
               float x[8];
 #pragma unroll
               for (int e = 0; e < 8; ++e) x[e] = l_run > 0.f ? __uint_as_float(o[8 * u + e]) : 0.f;
-              if (pieces == 1) pd_write8<T>(a, q.row0 + tok, head, c + 8 * u, x, inv);
+              if (pieces == 1) pd_write8<T>(a, q.row0 + tok, head, c + 8 * u, x, inv, gate[u]);
               else Row8<float>::store(a.part_o + slot_row * kD + c + 8 * u, x);
             }
           }

@@ -385,10 +385,6 @@ __device__ __forceinline__ FaTile fa_tile(const FaArgs& a, int pair, int rank) {
   return t;
 }
 
-// sigmoid(g) by the hardware's 2^x and reciprocal (2^-21 relative; the result is rounded to 16
-// bits at once, and the exact division's code would fill the instruction cache).
-__device__ __forceinline__ float fa_gate(float g) { return __fdividef(1.f, 1.f + attn_exp2(g * -1.4426950408889634f)); }
-
 // grid: 2 * pairs (head sets * an upper bound of the row blocks), clusters of 2; block: 384;
 // dynamic shared memory: kFaSmemBytes.
 template <typename T, bool kGate>
@@ -815,15 +811,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFaThreads, 1)
       float* part = a.part_o + (part_row + sub) * kD + 8 * chunk;
       if (a.parts > 1) a.part_ml[part_row + lane] = make_float2(m_run, l);
       if (!ok) break;
+      uint4 gate[8];  // of the dims of the pass, loaded a pass ahead
+      auto load_gate = [&](int c) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          gate[k] = 4 * k < rows_left ? __ldg(reinterpret_cast<const uint4*>(gsrc + 4 * k * a.ldg + c))
+                                      : make_uint4(0u, 0u, 0u, 0u);
+      };
+      if (kGate) load_gate(0);
 #pragma unroll 1
       for (int c = 0; c < kD; c += 64) {
-        uint4 gate[8];
-        if (kGate && a.parts == 1) {
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            gate[k] = 4 * k < rows_left ? __ldg(reinterpret_cast<const uint4*>(gsrc + 4 * k * a.ldg + c))
-                                        : make_uint4(0u, 0u, 0u, 0u);
-        }
         if (c == 0) {
           if (!(ok = wait(&fb.o_full, w & 1))) break;
           tc_fence_after();
@@ -856,13 +853,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFaThreads, 1)
               *reinterpret_cast<const float4*>(mine + i * 256 + (((2 * chunk) ^ (i & 15)) << 4));
           *reinterpret_cast<float4*>(y + 4) =
               *reinterpret_cast<const float4*>(mine + i * 256 + (((2 * chunk + 1) ^ (i & 15)) << 4));
-          if (kGate && a.parts == 1) {
+          if (kGate) {
             Row8<T> graw;
             graw.a = gate[k];
-            float gv[8];
-            graw.get(gv);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] *= fa_gate(gv[e]);
+            if (c + 64 < kD && 4 * k < rows_left)
+              gate[k] = __ldg(reinterpret_cast<const uint4*>(gsrc + 4 * k * a.ldg + c + 64));
+            gate_row8(graw, y);
           }
           if (4 * k < rows_left) {
             if (a.parts == 1) Row8<T>::store(dst + 4 * k * a.ldo + c, y);
@@ -907,6 +903,8 @@ __global__ void __launch_bounds__(256) prompt_join_kernel(FaArgs a) {
   const int idx = total - 1 - (before + at / block_rows);
   const int sets = a.by_heads ? a.hq / 2 : a.hq, set = a.by_heads ? head / 2 : head;
   const int rank = a.by_heads ? head & 1 : (at / kFaM) & 1;
+  Row8<T> graw;
+  if (a.gate) graw.load(static_cast<const T*>(a.gate) + row * a.ldg + head * kD + 8 * lane);
   float top = -INFINITY, l = 0.f, x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   for (int p = 0; p < a.parts; ++p) {
     const int64_t pair = (static_cast<int64_t>(idx) * a.parts + p) * sets + set;
@@ -925,14 +923,7 @@ __global__ void __launch_bounds__(256) prompt_join_kernel(FaArgs a) {
   const float inv = l > 0.f ? 1.f / l : 0.f;
 #pragma unroll
   for (int e = 0; e < 8; ++e) x[e] *= inv;
-  if (a.gate) {
-    Row8<T> graw;
-    graw.load(static_cast<const T*>(a.gate) + row * a.ldg + head * kD + 8 * lane);
-    float g[8];
-    graw.get(g);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] *= gate_factor(g[e]);
-  }
+  if (a.gate) gate_row8(graw, x);
   Row8<T>::store(static_cast<T*>(a.out) + row * a.ldo + head * kD + 8 * lane, x);
 }
 
