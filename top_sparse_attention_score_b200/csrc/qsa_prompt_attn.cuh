@@ -171,6 +171,16 @@ __device__ __forceinline__ void regs_grow() { asm volatile("setmaxnreg.inc.sync.
 template <int N>
 __device__ __forceinline__ void regs_shrink() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N)); }
 
+__device__ __forceinline__ void sts128(uint32_t addr, float x, float y, float z, float w) {
+  asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};\n" ::"r"(addr), "f"(x), "f"(y), "f"(z), "f"(w) : "memory");
+}
+__device__ __forceinline__ void lds128(uint32_t addr, float* v) {
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];\n"
+               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
+               : "r"(addr)
+               : "memory");
+}
+
 // One lane of a converged warp, the same one every time.
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
@@ -701,6 +711,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFaThreads, 1)
       if (lane == 0) mbar_arrive(&fb.tile_empty[w & 1]);
       if (!tile.live) break;
       const int seen = tile.seen0 + r;  // keys this row sees
+      if (kGate && g == 0 && r < tile.rows) {  // the row's gate into L2, for the end of the tile
+        const T* src = static_cast<const T*>(a.gate) + (static_cast<int64_t>(tile.row0) + r) * a.ldg + tile.head * kD;
+#pragma unroll
+        for (int c = 0; c < kD; c += 64) asm volatile("prefetch.global.L2 [%0];\n" ::"l"(src + c));
+      }
       const int ntiles = (tile.keys + kFaN - 1) / kFaN;
       float m_run = kFaNoMax, l_run = 0.f;
       for (int i = 0; i < ntiles; ++i, ++step) {
@@ -799,9 +814,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFaThreads, 1)
       if (lane == 0) mbar_arrive(&fb.l_free[quad]);
       // 32 rows x 64 dims at a time go through the warp's staging in fp32 (16-byte chunks
       // XOR-swizzled by the row): in, a lane has a row; out, eight lanes have 8 dims each of one
-      // row, so gate and output rows move in whole 128-byte lines.  The loop stays a loop: its
-      // code unrolled does not fit the instruction cache beside the softmax.
-      unsigned char* mine = stage + quad * (32 * 256);
+      // row, so gate and output rows move in whole 128-byte lines.  The loops stay loops: unrolled,
+      // their code does not fit the instruction cache beside the softmax, and a gated tile takes
+      // 24000 cycles to leave instead of a third of that.
+      const uint32_t mine = smem_u32(stage) + quad * (32 * 256);
+      const uint32_t in_row = mine + lane * 256 + ((lane & 15) << 4);  // chunk j at in_row ^ 16 j
       const int chunk = lane & 7, sub = lane >> 3;  // out: dims 8 chunk .. + 7 of rows 4 k + sub
       const int64_t first_row = tile.row0 + quad * 32 + sub;
       const int rows_left = tile.rows - quad * 32 - sub;
@@ -811,14 +828,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFaThreads, 1)
       float* part = a.part_o + (part_row + sub) * kD + 8 * chunk;
       if (a.parts > 1) a.part_ml[part_row + lane] = make_float2(m_run, l);
       if (!ok) break;
-      uint4 gate[8];  // of the dims of the pass, loaded a pass ahead
-      auto load_gate = [&](int c) {
+      Row8<T> gate[4];  // of the four rows that come next
+      auto load_gate = [&](int c, int k0) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          gate[k] = 4 * k < rows_left ? __ldg(reinterpret_cast<const uint4*>(gsrc + 4 * k * a.ldg + c))
-                                      : make_uint4(0u, 0u, 0u, 0u);
+        for (int k = 0; k < 4; ++k)
+          if (4 * (k0 + k) < rows_left) gate[k].load(gsrc + 4 * (k0 + k) * a.ldg + c);
       };
-      if (kGate) load_gate(0);
+      if (kGate) load_gate(0, 0);
 #pragma unroll 1
       for (int c = 0; c < kD; c += 64) {
         if (c == 0) {
@@ -836,34 +852,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFaThreads, 1)
         }
         __syncwarp();
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          float4 v;  // O of a row that saw nothing may be anything
-          v.x = l > 0.f ? __uint_as_float(o[4 * j]) * inv : 0.f;
-          v.y = l > 0.f ? __uint_as_float(o[4 * j + 1]) * inv : 0.f;
-          v.z = l > 0.f ? __uint_as_float(o[4 * j + 2]) * inv : 0.f;
-          v.w = l > 0.f ? __uint_as_float(o[4 * j + 3]) * inv : 0.f;
-          *reinterpret_cast<float4*>(mine + lane * 256 + ((j ^ (lane & 15)) << 4)) = v;
+        for (int j = 0; j < 16; ++j)
+          sts128(in_row ^ (j << 4), __uint_as_float(o[4 * j]) * inv, __uint_as_float(o[4 * j + 1]) * inv,
+                 __uint_as_float(o[4 * j + 2]) * inv, __uint_as_float(o[4 * j + 3]) * inv);
+        if (!(l > 0.f)) {  // O of a row that saw nothing may be anything
+#pragma unroll 1
+          for (int j = 0; j < 16; ++j) sts128(in_row ^ (j << 4), 0.f, 0.f, 0.f, 0.f);
         }
         __syncwarp();
+#pragma unroll 1
+        for (int k0 = 0; k0 < 8; k0 += 4) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int i = 4 * k + sub;
-          float y[8];
-          *reinterpret_cast<float4*>(y) =
-              *reinterpret_cast<const float4*>(mine + i * 256 + (((2 * chunk) ^ (i & 15)) << 4));
-          *reinterpret_cast<float4*>(y + 4) =
-              *reinterpret_cast<const float4*>(mine + i * 256 + (((2 * chunk + 1) ^ (i & 15)) << 4));
-          if (kGate) {
-            Row8<T> graw;
-            graw.a = gate[k];
-            if (c + 64 < kD && 4 * k < rows_left)
-              gate[k] = __ldg(reinterpret_cast<const uint4*>(gsrc + 4 * k * a.ldg + c + 64));
-            gate_row8(graw, y);
+          for (int k = 0; k < 4; ++k) {
+            const int i = 4 * (k0 + k) + sub;
+            float y[8];
+            lds128(mine + i * 256 + (((2 * chunk) ^ (i & 15)) << 4), y);
+            lds128(mine + i * 256 + (((2 * chunk + 1) ^ (i & 15)) << 4), y + 4);
+            if (kGate) gate_row8(gate[k], y);
+            if (4 * (k0 + k) < rows_left) {
+              if (a.parts == 1) Row8<T>::store(dst + 4 * (k0 + k) * a.ldo + c, y);
+              else Row8<float>::store(part + 4 * (k0 + k) * kD + c, y);
+            }
           }
-          if (4 * k < rows_left) {
-            if (a.parts == 1) Row8<T>::store(dst + 4 * k * a.ldo + c, y);
-            else Row8<float>::store(part + 4 * k * kD + c, y);
-          }
+          if (kGate && (k0 == 0 || c + 64 < kD)) load_gate(k0 == 0 ? c : c + 64, 4 - k0);
         }
       }
     }
