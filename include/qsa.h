@@ -354,8 +354,9 @@ size_t qsa_paged_decode_workspace_bytes(int nseq, int hq, int hkv, int max_q, in
  *   ws       at least qsa_paged_decode_workspace_bytes(...) bytes, one call at a time
  * Requires max_q * hq / hkv <= 96.  The result does not depend on how the cells are split
  * beyond rounding and is the same in every run.  fp16 / bf16: q and the weights enter the
- * tensor cores as fp16, V as fp16(code * scale); fp32: each as a pair of fp16 (22 bits).  So
- * |q| and |V| up to 65504 are held; accumulation and the softmax are fp32.
+ * tensor cores as fp16, K and V as fp16(code * scale); fp32: q, the weights and V as pairs of
+ * fp16 (22 bits), K's codes exactly.  So |q|, |K| and |V| up to 65504 are held; accumulation and
+ * the softmax are fp32.  scale is positive and finite, here and in qsa_prompt_attn.
  */
 int qsa_paged_decode(const qsa_paged_cache* cache, const qsa_batch* batch, int rows, int max_q,
                      int max_len, int dtype, int hq, const void* q, int64_t ldq, const void* gate,

@@ -441,3 +441,106 @@ def test_write_then_decode_then_read(gpu):
     kk, _ = qsa.paged_read(c.cache, c.batch, 6, torch.float32)
     codes, s = quantise(k.float().cpu().numpy())
     assert np.array_equal(kk.cpu().numpy(), codes.astype(np.float32) * np.repeat(s.astype(np.float32), 32, -1))
+
+
+@pytest.mark.parametrize("dtype,n", [(torch.float32, 1), (torch.bfloat16, 1), (torch.float16, 3)])
+def test_pages_far_into_the_pool(gpu, dtype, n):
+    """Byte offsets past 2^32: a pool of 9 million cells whose last pages are in use."""
+    qsa = gpu
+    pages, page, L = 70000, 128, 300
+    cache = qsa.PagedCache.empty(pages, page, 2, DEV)
+    table = torch.tensor([[pages - 1, 3, pages - 2]], dtype=torch.int32, device=DEV)
+    kv_len = torch.tensor([L], dtype=torch.int32, device=DEV)
+    k, v = draw_rows(40, (L, 2, D), dtype), draw_rows(41, (L, 2, D), dtype)
+    whole = qsa.Batch(table, kv_len, torch.tensor([0, L], dtype=torch.int32, device=DEV))
+    qsa.paged_write(cache, whole, k, v)
+    kk, vv = qsa.paged_read(cache, whole, L, torch.float32)
+    for x, got in ((k, kk), (v, vv)):
+        codes, s = quantise(x.float().cpu().numpy())
+        assert np.array_equal(got.cpu().numpy(), codes.astype(np.float32) * np.repeat(s.astype(np.float32), 32, -1))
+    q = draw_rows(42, (n, 24, D), dtype)
+    new = qsa.Batch(table, kv_len, torch.tensor([0, n], dtype=torch.int32, device=DEV))
+    out = qsa.paged_decode(cache, new, q, max_q=n).double().cpu().numpy()
+    kd, vd = kk.double().cpu().numpy(), vv.double().cpu().numpy()
+    ref, mag = attention(q.double().cpu().numpy(), kd, vd, 1 / 16)
+    norm = float(q.double().norm(dim=-1).max()) * np.abs(kd).max()   # |q o k| <= |q| max|k|
+    extra = 0 if dtype == torch.float32 else 6 * 2.0 ** -11 / 3 ** 0.5 / 16 * norm
+    assert (np.abs(out - ref) / mag).max() <= TOL[dtype] + extra
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_decode_rows_past_max_q_stay(gpu, dtype):
+    """A sequence with more rows than max_q: its first max_q rows are computed, the others stay."""
+    qsa = gpu
+    c = Case(qsa, [100, 50], [4, 2], page=16, hkv=2, seed=24)
+    q = draw_rows(1, (6, 24, D), dtype)
+    want = qsa.paged_decode(c.cache, c.batch, q, max_q=4)
+    out = torch.full_like(q, 7.0)
+    qsa.paged_decode(c.cache, c.batch, q, max_q=2, out=out)
+    assert torch.all(out[2:4] == 7.0)
+    for r in (0, 1, 4, 5):
+        assert (out[r].double() - want[r].double()).abs().max() <= 4 * TOL[dtype] * want[r].double().abs().max()
+
+
+def test_decode_length_past_the_table(gpu):
+    """Positions that the table does not reach, or past max_len, are not attended."""
+    qsa = gpu
+    c = Case(qsa, [64, 64], [1, 1], page=16, hkv=2, seed=25)
+    q = draw_rows(2, (2, 24, D), torch.float32)
+    want = qsa.paged_decode(c.cache, c.batch, q)
+    longer = qsa.Batch(c.batch.table, c.ints([1000, 64]), c.batch.cu_q)
+    assert torch.equal(qsa.paged_decode(c.cache, longer, q), want)
+    short = qsa.paged_decode(c.cache, qsa.Batch(c.batch.table, c.ints([48, 64]), c.batch.cu_q), q)
+    cut = qsa.paged_decode(c.cache, c.batch, q, max_len=48)
+    assert torch.equal(cut[0], short[0])
+
+
+def test_calls_on_two_streams_at_once(gpu):
+    """Calls of all kinds on two streams, each with its own workspace, beside each other."""
+    qsa = gpu
+    c = Case(qsa, [5000, 1200, 333], [3, 3, 3], page=64, hkv=2, seed=26)
+    q16, q32 = draw_rows(3, (9, 24, D), torch.bfloat16), draw_rows(4, (9, 24, D), torch.float32)
+    pq, pk, pv = (draw_rows(i, (700, h, D), torch.bfloat16) for i, h in ((5, 24), (6, 2), (7, 2)))
+    cu = c.ints([0, 700])
+    calls = [lambda s: qsa.paged_decode(c.cache, c.batch, q16, max_q=3, stream=s),
+             lambda s: qsa.paged_decode(c.cache, c.batch, q32, max_q=3, stream=s),
+             lambda s: qsa.prompt_attn(pq, pk, pv, cu, stream=s),
+             lambda s: qsa.prompt_attn(pq[:40].contiguous(), pk, pv, c.ints([0, 40]), cu, stream=s),
+             lambda s: qsa.paged_read(c.cache, c.batch, 9, torch.float16, stream=s)[0]]
+    want = [f(None) for f in calls]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[] for _ in calls]
+    for rep in range(4):
+        for i, f in enumerate(calls):
+            got[i].append(f(streams[(i + rep) % 2]))
+    torch.cuda.synchronize()
+    for w, g in zip(want, got):
+        assert all(torch.equal(w, x) for x in g)
+    assert qsa.device_status() == 0
+
+
+def test_binding_refusals_on_the_gpu(gpu):
+    """Shapes, types, strides, devices that the binding refuses; nothing is launched."""
+    qsa = gpu
+    c = Case(qsa, [40, 20], [1, 1], page=16, hkv=2, seed=27)
+    q = draw_rows(1, (2, 24, D), torch.float16)
+    before = qsa.launch_count()
+    for args in (dict(q=q.cpu()), dict(q=q[:, :, :128]), dict(q=q.double()), dict(gate=q.float()), dict(gate=q[:1]),
+                 dict(out=q[:1]), dict(ws=torch.empty(16, dtype=torch.uint8))):
+        a = dict(q=q)
+        a.update(args)
+        with pytest.raises(ValueError):
+            qsa.paged_decode(c.cache, c.batch, a.pop("q"), **a)
+    with pytest.raises(qsa.QSAError, match="WORKSPACE"):
+        qsa.paged_decode(c.cache, c.batch, q, ws=torch.empty(64, dtype=torch.uint8, device=DEV))
+    with pytest.raises(qsa.QSAError, match="multiple"):
+        qsa.paged_decode(c.cache, c.batch, draw_rows(1, (2, 23, D), torch.float16))
+    with pytest.raises(ValueError):
+        qsa.paged_write(c.cache, c.batch, q[:, :2], q[:, :3])
+    with pytest.raises(ValueError):
+        qsa.Batch(c.batch.table, c.batch.kv_len[:1])
+    with pytest.raises(qsa.QSAError, match="QSA_F16"):
+        x = q.float()
+        qsa.prompt_attn(x, x, x, c.ints([0, 2]))
+    assert qsa.launch_count() == before

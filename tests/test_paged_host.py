@@ -56,10 +56,10 @@ def test_write_and_read_refuse(lib, fn):
 
 
 def decode(lib, c=None, b=None, rows=5, max_q=2, max_len=64, dtype=0, hq=24, q=P, ldq=24 * 256, gate=None, ldg=0, ws=P,
-           ws_bytes=1 << 40, out=P, ldo=24 * 256):
+           ws_bytes=1 << 40, out=P, ldo=24 * 256, scale=0.0625):
     c, b = c or paged(), b or batch()
     return lib.qsa_paged_decode(ctypes.byref(c), ctypes.byref(b), rows, max_q, max_len, dtype, hq, q, ldq, gate, ldg,
-                                0.0625, ws, ws_bytes, out, ldo, None)
+                                scale, ws, ws_bytes, out, ldo, None)
 
 
 def test_decode_refuses(lib):
@@ -76,6 +76,9 @@ def test_decode_refuses(lib):
     assert decode(lib, q=P + 2) == ARG
     assert decode(lib, out=None) == ARG
     assert decode(lib, gate=P, ldg=100) == ARG and "gate" in qsa.last_error()
+    for scale in (0.0, -0.0625, float("nan"), float("inf")):
+        assert decode(lib, scale=scale) == ARG and "scale" in qsa.last_error()
+        assert prompt(lib, scale=scale) == ARG and "scale" in qsa.last_error()
     assert decode(lib, ws=None) == WORKSPACE
     assert decode(lib, ws=P + 8) == ARG
     assert decode(lib, rows=0, q=None, out=None) == OK
@@ -90,8 +93,8 @@ def test_decode_workspace(lib):
 
 
 def prompt(lib, nseq=2, cu_q=P, cu_k=P, rows_q=300, rows_k=300, dtype=2, hq=24, hkv=2, q=P, ldq=24 * 256, k=P, ldk=512,
-           v=P, ldv=512, gate=None, ldg=0, ws=P, ws_bytes=1 << 40, out=P, ldo=24 * 256):
-    return lib.qsa_prompt_attn(nseq, cu_q, cu_k, rows_q, rows_k, dtype, hq, hkv, q, ldq, k, ldk, v, ldv, gate, ldg, 0.0625,
+           v=P, ldv=512, gate=None, ldg=0, ws=P, ws_bytes=1 << 40, out=P, ldo=24 * 256, scale=0.0625):
+    return lib.qsa_prompt_attn(nseq, cu_q, cu_k, rows_q, rows_k, dtype, hq, hkv, q, ldq, k, ldk, v, ldv, gate, ldg, scale,
                                ws, ws_bytes, out, ldo, None)
 
 

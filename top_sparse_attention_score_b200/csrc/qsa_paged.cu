@@ -90,13 +90,19 @@ cudaError_t launch_read(const qsa::PagedBatch& b, const qsa::PagedCells& c, int 
                     dim3(32 * qsa::kPagedWarps), 0, s, b, c, rows, static_cast<T*>(k), static_cast<T*>(v), ldk, ldv);
 }
 
+// A positive finite softmax scale (the kernels take a tile's largest score before they scale it).
+int check_scale(float scale) {
+  if (!(scale > 0.f) || scale > 3.0e38f) return fail(QSA_ERR_ARG, "scale = %g must be positive and finite", scale);
+  return QSA_OK;
+}
+
 // ---- decode plan
 
 // Kernel shape for a call's rows.  fp32 calls (split), and fp16 / bf16 calls of at most 16 rows:
 // the tiles of 16 query rows (warps of a group) and the groups of a CTA, two CTAs per SM where
 // registers and shared memory allow.  fp16 / bf16 calls of more rows: the tcgen05 kernel, one CTA
 // per SM, blocks of 64 cells whatever the rows.  2 x 131072 cells of 2 KV heads, 12 rows a token:
-// one token 86 us on the first and 119 on the second, two 147 and 119, eight 491 and 128.
+// one token 84 us on the first and 96 on the second, two 147 and 96, eight 491 and 104.
 struct DecodePlan {
   int mt, groups, ctas_per_sm, prows, block_cells;
   bool tc;  // the tcgen05 kernel
@@ -136,33 +142,43 @@ int check_decode_sizes(int nseq, int hq, int hkv, int max_q, int64_t max_len) {
   return QSA_OK;
 }
 
-// Launch with the kernel's dynamic shared memory opted in to, once per device (`done`: its mask).
+// Opt the kernel in to its dynamic shared memory, once per device (`done`: the devices' mask).
+// `regs` > 0: the registers a thread that its warpgroups share out; a build with others would
+// wait for registers that the block does not have, so it is not launched.
 template <typename K>
-cudaError_t launch_big(K kernel, std::atomic<uint64_t>& done, int grid, int threads, int smem, const qsa::PdArgs& a,
-                       cudaStream_t s) {
+cudaError_t opt_in(K kernel, std::atomic<uint64_t>& done, int smem, int regs) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const uint64_t bit = 1ull << (dev & 63);
-  if (!(done.load(std::memory_order_relaxed) & bit)) {
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    done.fetch_or(bit, std::memory_order_relaxed);
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  if (regs > 0) {
+    cudaFuncAttributes fa;
+    if ((e = cudaFuncGetAttributes(&fa, kernel)) != cudaSuccess) return e;
+    if (fa.numRegs != regs) return cudaErrorInvalidKernelImage;
   }
-  return launch_pdl(kernel, dim3(grid), dim3(threads), smem, s, a);
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
 }
 
 template <typename T, int MT, int C, int STAGES, int MINB>
 cudaError_t launch_decode_mma(const qsa::PdArgs& a, int grid, cudaStream_t s) {
   static std::atomic<uint64_t> done{0};
-  return launch_big(qsa::paged_decode_kernel<T, MT, C, STAGES, MINB>, done, grid, 32 * qsa::kPdW * MT * C,
-                    qsa::PdSmem<MT, C, STAGES, sizeof(T) == 4>::kBytes, a, s);
+  auto kernel = qsa::paged_decode_kernel<T, MT, C, STAGES, MINB>;
+  constexpr int smem = qsa::PdSmem<MT, C, STAGES, sizeof(T) == 4>::kBytes;
+  const cudaError_t e = opt_in(kernel, done, smem, 0);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kernel, dim3(grid), dim3(32 * qsa::kPdW * MT * C), smem, s, a);
 }
 
 template <typename T>
 cudaError_t launch_decode_tc(const qsa::PdArgs& a, int grid, cudaStream_t s) {
   static std::atomic<uint64_t> done{0};
-  return launch_big(qsa::paged_decode_tc_kernel<T>, done, grid, qsa::kTdThreads, qsa::kTdSmemBytes, a, s);
+  auto kernel = qsa::paged_decode_tc_kernel<T>;
+  const cudaError_t e = opt_in(kernel, done, qsa::kTdSmemBytes, qsa::kTdRegsLaunch);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kernel, dim3(grid), dim3(qsa::kTdThreads), qsa::kTdSmemBytes, s, a);
 }
 
 template <typename T>
@@ -256,17 +272,10 @@ int check_prompt_sizes(int nseq, int rows_q, int rows_k, int hq, int hkv) {
 template <typename T, bool kGate>
 cudaError_t launch_prompt(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const qsa::FaArgs& a,
                           int pairs, cudaStream_t s) {
-  auto kernel = qsa::prompt_attn_kernel<T, kGate>;
   static std::atomic<uint64_t> done{0};
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  auto kernel = qsa::prompt_attn_kernel<T, kGate>;
+  const cudaError_t e = opt_in(kernel, done, qsa::kFaSmemBytes, qsa::kFaRegsLaunch);
   if (e != cudaSuccess) return e;
-  const uint64_t bit = 1ull << (dev & 63);
-  if (!(done.load(std::memory_order_relaxed) & bit)) {
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, qsa::kFaSmemBytes);
-    if (e != cudaSuccess) return e;
-    done.fetch_or(bit, std::memory_order_relaxed);
-  }
   return launch_pdl(kernel, dim3(2 * pairs), dim3(qsa::kFaThreads), qsa::kFaSmemBytes, s, q, k, v, a);
 }
 
@@ -333,6 +342,7 @@ int qsa_paged_decode(const qsa_paged_cache* cache, const qsa_batch* batch, int r
   if (r) return r;
   if ((r = check_dtype(dtype))) return r;
   if ((r = check_decode_sizes(batch->nseq, hq, cache->hkv, max_q, max_len))) return r;
+  if ((r = check_scale(scale))) return r;
   if (rows == 0) return ok();
   if ((r = check_rows("q", q, ldq, hq, dtype)) || (r = check_rows("out", out, ldo, hq, dtype)) ||
       (gate && (r = check_rows("gate", gate, ldg, hq, dtype))))
@@ -386,6 +396,7 @@ int qsa_prompt_attn(int nseq, const int32_t* cu_q, const int32_t* cu_k, int rows
     return fail(QSA_ERR_ARG, "dtype = %d: prompt attention takes QSA_F16 or QSA_BF16 rows", dtype);
   if ((r = check_prompt_sizes(nseq, rows_q, rows_k, hq, hkv))) return r;
   if (!cu_q || !cu_k) return fail(QSA_ERR_ARG, "cu_q and cu_k must not be NULL");
+  if ((r = check_scale(scale))) return r;
   if (rows_q == 0) return ok();
   if ((r = check_rows("q", q, ldq, hq, dtype)) || (r = check_rows("out", out, ldo, hq, dtype)) ||
       (gate && (r = check_rows("gate", gate, ldg, hq, dtype))))
@@ -418,6 +429,7 @@ int qsa_prompt_attn(int nseq, const int32_t* cu_q, const int32_t* cu_k, int rows
   a.group = hq / hkv;
   a.by_heads = p.by_heads;
   a.parts = p.parts;
+  a.pairs = static_cast<int>(p.pairs);
   a.part_o = reinterpret_cast<float*>(static_cast<char*>(ws) + p.part_o);
   a.part_ml = reinterpret_cast<float2*>(static_cast<char*>(ws) + p.part_ml);
   a.scale_log2 = scale * 1.4426950408889634f;

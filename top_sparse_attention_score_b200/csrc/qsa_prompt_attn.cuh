@@ -101,6 +101,7 @@ struct FaArgs {
   int hq, group;
   int by_heads;  // a pair is two heads (else two blocks of rows)
   int parts;     // pieces of a tile's keys, each a tile of its own, joined afterwards
+  int pairs;     // of the grid
   float* part_o;    // parts > 1: [pairs of the grid][2][128][256] unnormalised rows
   float2* part_ml;  // [pairs of the grid][2][128]: reference (log2 units), sum
   float scale_log2;
@@ -919,6 +920,7 @@ __global__ void __launch_bounds__(256) prompt_join_kernel(FaArgs a) {
   float top = -INFINITY, l = 0.f, x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   for (int p = 0; p < a.parts; ++p) {
     const int64_t pair = (static_cast<int64_t>(idx) * a.parts + p) * sets + set;
+    if (pair < 0 || pair >= a.pairs) break;  // cu_q was not ascending: more blocks than rows allow
     const int64_t r = (2 * pair + rank) * kFaM + at % kFaM;
     const float2 ml = __ldcg(a.part_ml + r);
     if (!(ml.y > 0.f)) continue;  // the part saw nothing (its rows hold anything)
