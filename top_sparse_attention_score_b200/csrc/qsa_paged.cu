@@ -232,7 +232,7 @@ struct PromptPlan {
 // shorter by this estimate in key tiles (1.5 us each on the device): rounds of `pairs_at_once`
 // pairs, a tile's fixed cost of about four key tiles, and a part's rows written and read again
 // (two thirds of a microsecond for a hundred pairs) with one more launch.  16 rows of 24 heads at
-// 32768 keys: 12 pairs of 256 key tiles, 437 us whole and 70 us in 12 parts.
+// 32768 keys: 12 pairs of 256 key tiles, 437 us whole; in parts 76 us and 10 us to join.
 PromptPlan plan_prompt(int nseq, int rows_q, int rows_k, int hq, int hkv) {
   PromptPlan p;
   constexpr int pairs_at_once = 74;

@@ -3,11 +3,12 @@
 // Mathematics, flat work list and partial slots are those of qsa_paged_decode.cuh; the query
 // rows of a sequence and KV head (tokens x heads, at most 96) are rows of one 128-row tile.
 //
-// Bound: HBM.  Turning a cell's 512 codes into fp16 is what the issue slots go to (about 35 warp
+// Floor: HBM.  Turning a cell's 512 codes into fp16 is what the issue slots go to (about 35 warp
 // instructions a cell of the 93 that HBM's rate leaves), and mma.sync needs them again for every
-// 16 rows and holds O in registers (8 warps an SM: 86 us for 2 x 131072 cells and one token,
-// 256 us for four).  Here sixteen warps do nothing else, the products cost no issue slots, and
-// their cost does not depend on the rows.  One CTA per SM:
+// 16 rows (2 x 131072 cells of 2 KV heads, 12 rows a token: 84 us for one token, 147 for two, 491
+// for eight).  Here sixteen warps do nothing else, the products cost no issue slots, and their
+// cost does not depend on the rows: 96 us for one or two tokens, 104 for eight (43.5 at HBM's
+// rate).  The conversion warps' latency and the shared-memory path bound it.  One CTA per SM:
 //   * sixteen warps fetch and convert, eight each of the even and the odd blocks: a lane loads 16
 //     codes at a time, makes them fp16(code * scale) and stores them into the K or V tile of 64
 //     cells (128-byte swizzle; the same layout serves K as a K-major and V as an MN-major
