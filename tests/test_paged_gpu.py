@@ -385,6 +385,23 @@ def test_decode_stale_cells_do_not_matter(gpu):
     assert torch.equal(a, b) and torch.isfinite(b).all()
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("lens", [[40], [6000]])
+@pytest.mark.parametrize("n", [1, 3])
+def test_decode_nan_rows_stay_nan(gpu, dtype, lens, n):
+    """A NaN query gives NaN in its own row and head alone: in whole and in joined pieces."""
+    qsa = gpu
+    c = Case(qsa, lens, [n], page=16, hkv=2, seed=23)
+    q = draw_rows(9, (n, 24, D), dtype)
+    want = qsa.paged_decode(c.cache, c.batch, q, max_q=n, max_len=lens[0])
+    q[0, 5, 100] = float("nan")
+    got = qsa.paged_decode(c.cache, c.batch, q, max_q=n, max_len=lens[0])
+    torch.cuda.synchronize()
+    assert torch.isnan(got[0, 5]).all()
+    got[0, 5] = want[0, 5]
+    assert torch.equal(got, want)
+
+
 def test_decode_runs_are_equal_and_strides(gpu):
     """The same bits in every run; q, gate and out as slices of wider rows."""
     qsa = gpu

@@ -152,6 +152,29 @@ def test_prompt_neighbours_do_not_matter(gpu):
     assert torch.equal(got[100:230], want[100:230])
 
 
+@pytest.mark.parametrize("rows,keys,split", [(300, 300, False), (40, 9000, True)])
+def test_prompt_keys_to_come_do_not_matter(gpu, rows, keys, split):
+    """A row's result does not change with the keys behind it: NaN and infinite K, other V."""
+    qsa = gpu
+    g = torch.Generator(device=DEV).manual_seed(61)
+    q = torch.randn(rows, 4, D, generator=g, device=DEV).to(torch.bfloat16)
+    kv = torch.randn(2, keys, 2, D, generator=g, device=DEV).to(torch.bfloat16)
+    cq = torch.tensor([0, rows], dtype=torch.int32, device=DEV)
+    ck = torch.tensor([0, keys], dtype=torch.int32, device=DEV)
+    assert (qsa.prompt_attn_workspace_bytes(1, rows, keys, 4, 2) > 0) == split
+    want = qsa.prompt_attn(q, kv[0], kv[1], cq, ck)
+    seen = rows // 2  # the first rows, and the keys that the last of them sees
+    other = kv.clone()
+    last = keys - rows + seen
+    other[0, last:] = float("nan")
+    other[0, last + 1::2] = float("inf")
+    other[1, last:] = 30000.0
+    got = qsa.prompt_attn(q, other[0], other[1], cq, ck)
+    torch.cuda.synchronize()
+    assert torch.equal(got[:seen], want[:seen])
+    assert not torch.isfinite(got[seen:]).any()
+
+
 def test_prompt_runs_are_equal_and_on_another_stream(gpu):
     qsa = gpu
     cu = ints([0, 500, 900])

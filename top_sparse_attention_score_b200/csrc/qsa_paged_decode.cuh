@@ -71,7 +71,7 @@ struct PdArgs {
 // Rows and cells of sequence s as this call sees them.
 struct PdSeq {
   int row0;  // first packed row
-  int n;     // its rows, at most max_q
+  int n;     // its rows (those past max_q are not computed)
   int len;   // true length (visibility)
   int cells; // cells to visit
 };
@@ -481,7 +481,8 @@ __global__ void __launch_bounds__(32 * kPdW * MT * C, MINB) paged_decode_kernel(
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       const int row = (cg * MT + mt) * 16 + g + 8 * r;
-      if (t == 0 && dh == 0) sstat[row] = make_float2(l_run[r] > 0.f ? m_run[r] : -INFINITY, l_run[r]);
+      // a sum is 0 where the row saw nothing, and NaN (to be passed on) where a score was
+      if (t == 0 && dh == 0) sstat[row] = make_float2(l_run[r] != 0.f ? m_run[r] : -INFINITY, l_run[r]);
 #pragma unroll
       for (int gi = 0; gi < kPdG; ++gi) {
         // C element (row, col 2t) of n-tile i, group gi is dim 32 gi + 8 t + i; col 2t+1 is +4
@@ -507,7 +508,7 @@ __global__ void __launch_bounds__(32 * kPdW * MT * C, MINB) paged_decode_kernel(
       }
 #pragma unroll
       for (int c = 0; c < C; ++c) {
-        const float w = st[c].y > 0.f ? attn_exp2(st[c].x - top) : 0.f;
+        const float w = st[c].y != 0.f ? attn_exp2(st[c].x - top) : 0.f;
         l = fmaf(w, st[c].y, l);
         const float4* src = reinterpret_cast<const float4*>(sjoin + (c * MT * 16 + row) * kRow + 8 * lane);
         const float4 lo = src[0], hi = src[1];
@@ -515,7 +516,7 @@ __global__ void __launch_bounds__(32 * kPdW * MT * C, MINB) paged_decode_kernel(
         x[4] = fmaf(w, hi.x, x[4]), x[5] = fmaf(w, hi.y, x[5]), x[6] = fmaf(w, hi.z, x[6]), x[7] = fmaf(w, hi.w, x[7]);
       }
       if (pieces == 1) {
-        pd_write8<T>(a, q.row0 + tok, head, 8 * lane, x, l > 0.f ? 1.f / l : 0.f, gate);
+        pd_write8<T>(a, q.row0 + tok, head, 8 * lane, x, l != 0.f ? 1.f / l : 0.f, gate);
       } else {
         Row8<float>::store(a.part_o + (slot_row + row) * kD + 8 * lane, x);
         if (lane == 0) a.part_ml[slot_row + row] = make_float2(top, l);
@@ -581,7 +582,7 @@ __global__ void __launch_bounds__(32 * kPjWarps) paged_join_kernel(PdArgs a) {
     for (int e = 0; e < 8; ++e) x[e] *= alpha;
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      const float w = ml[u].y > 0.f ? attn_exp2(ml[u].x - mnew) : 0.f;
+      const float w = ml[u].y != 0.f ? attn_exp2(ml[u].x - mnew) : 0.f;
       l = fmaf(w, ml[u].y, l);
       x[0] = fmaf(w, lo[u].x, x[0]), x[1] = fmaf(w, lo[u].y, x[1]);
       x[2] = fmaf(w, lo[u].z, x[2]), x[3] = fmaf(w, lo[u].w, x[3]);
@@ -600,12 +601,12 @@ __global__ void __launch_bounds__(32 * kPjWarps) paged_join_kernel(PdArgs a) {
   for (int e = 0; e < 8; ++e) x[e] = 0.f;
 #pragma unroll
   for (int w = 0; w < kPjWarps; ++w) {
-    const float e = sl[w] > 0.f ? attn_exp2(sm[w] - all) : 0.f;
+    const float e = sl[w] != 0.f ? attn_exp2(sm[w] - all) : 0.f;
     total = fmaf(e, sl[w], total);
 #pragma unroll
     for (int i = 0; i < 8; ++i) x[i] = fmaf(e, so[w][8 * lane + i], x[i]);
   }
-  pd_write8<T>(a, row, head, 8 * lane, x, total > 0.f ? 1.f / total : 0.f, gate);
+  pd_write8<T>(a, row, head, 8 * lane, x, total != 0.f ? 1.f / total : 0.f, gate);
 }
 
 }  // namespace qsa

@@ -468,7 +468,8 @@ __global__ void __launch_bounds__(kTdThreads, 1) paged_decode_tc_kernel(PdArgs a
       // ---------------- the piece's rows: final, or a partial
       ok = ok && wait(&tb.o_full, piece & 1);
       tc_fence_after();
-      const float inv = l_run > 0.f ? 1.f / l_run : 0.f;
+      // 0: the row saw nothing; NaN is passed on
+      const float inv = l_run != 0.f ? 1.f / l_run : 0.f;
       const int tok = r / a.group, head = kvh * a.group + r - tok * a.group;
       const size_t slot_row = (2 * static_cast<size_t>(blockIdx.x) + (blk0 == 0 ? 1 : 0)) * a.prows + r;
       if (warp * 32 < nrow) {
@@ -487,14 +488,14 @@ __global__ void __launch_bounds__(kTdThreads, 1) paged_decode_tc_kernel(PdArgs a
             for (int u = 0; u < 4; ++u) {
               float x[8];
 #pragma unroll
-              for (int e = 0; e < 8; ++e) x[e] = l_run > 0.f ? __uint_as_float(o[8 * u + e]) : 0.f;
+              for (int e = 0; e < 8; ++e) x[e] = l_run != 0.f ? __uint_as_float(o[8 * u + e]) : 0.f;
               if (pieces == 1) pd_write8<T>(a, q.row0 + tok, head, c + 8 * u, x, inv, gate[u]);
               else Row8<float>::store(a.part_o + slot_row * kD + c + 8 * u, x);
             }
           }
           __syncwarp();
         }
-        if (pieces > 1 && r < nrow) a.part_ml[slot_row] = make_float2(l_run > 0.f ? m_run : -INFINITY, l_run);
+        if (pieces > 1 && r < nrow) a.part_ml[slot_row] = make_float2(l_run != 0.f ? m_run : -INFINITY, l_run);
       }
       tc_fence_before();
       __syncwarp();

@@ -815,7 +815,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFaThreads, 1)
       // ---------------- the other one reads O out: O / l, gated
       ok = ok && wait(&fb.l_full[quad], w & 1);
       const float l = l_run + fb.l_part[r];
-      const float inv = a.parts > 1 ? 1.f : 1.f / l;  // used where l > 0
+      const float inv = a.parts > 1 ? 1.f : 1.f / l;  // used where l != 0
       __syncwarp();
       if (lane == 0) mbar_arrive(&fb.l_free[quad]);
       // 32 rows x 64 dims at a time go through the warp's staging in fp32 (16-byte chunks
@@ -861,7 +861,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFaThreads, 1)
         for (int j = 0; j < 16; ++j)
           sts128(in_row ^ (j << 4), __uint_as_float(o[4 * j]) * inv, __uint_as_float(o[4 * j + 1]) * inv,
                  __uint_as_float(o[4 * j + 2]) * inv, __uint_as_float(o[4 * j + 3]) * inv);
-        if (!(l > 0.f)) {  // O of a row that saw nothing may be anything
+        if (l == 0.f) {  // O of a row that saw nothing may be anything; a NaN sum is passed on
 #pragma unroll 1
           for (int j = 0; j < 16; ++j) sts128(in_row ^ (j << 4), 0.f, 0.f, 0.f, 0.f);
         }
@@ -928,7 +928,7 @@ __global__ void __launch_bounds__(256) prompt_join_kernel(FaArgs a) {
     if (pair < 0 || pair >= a.pairs) break;  // cu_q was not ascending: more blocks than rows allow
     const int64_t r = (2 * pair + rank) * kFaM + at % kFaM;
     const float2 ml = __ldcg(a.part_ml + r);
-    if (!(ml.y > 0.f)) continue;  // the part saw nothing (its rows hold anything)
+    if (ml.y == 0.f) continue;  // the part saw nothing (its rows hold anything)
     const float mnew = fmaxf(top, ml.x), w = attn_exp2(ml.x - mnew), keep = attn_exp2(top - mnew);
     top = mnew;
     l = fmaf(l, keep, w * ml.y);
@@ -938,7 +938,7 @@ __global__ void __launch_bounds__(256) prompt_join_kernel(FaArgs a) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) x[e] = fmaf(x[e], keep, w * y[e]);
   }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
+  const float inv = l != 0.f ? 1.f / l : 0.f;
 #pragma unroll
   for (int e = 0; e < 8; ++e) x[e] *= inv;
   if (a.gate) gate_row8(graw, x);
