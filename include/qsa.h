@@ -279,7 +279,7 @@ int qsa_topk_static(const float* scores, int64_t ld, int rows, int vis0, int top
  * counts are free (query head h uses KV head h / (hq / hkv)).  Rows are fp32, fp16 or bf16
  * ("dtype": one type for a call's inputs and outputs), each row's heads contiguous, rows `ld`
  * elements apart (ld * element size a multiple of 16 bytes), so a slice of a wider projection
- * row needs no copy.
+ * row needs no copy.  Outputs and workspaces overlap no other argument of a call.
  */
 
 /*
@@ -356,7 +356,7 @@ size_t qsa_paged_decode_workspace_bytes(int nseq, int hq, int hkv, int max_q, in
  * beyond rounding and is the same in every run.  fp16 / bf16: q and the weights enter the
  * tensor cores as fp16, K and V as fp16(code * scale); fp32: q, the weights and V as pairs of
  * fp16 (22 bits), K's codes exactly.  So |q|, |K| and |V| up to 65504 are held; accumulation and
- * the softmax are fp32.  scale is positive and finite, here and in qsa_prompt_attn.
+ * the softmax are fp32.  0 < scale <= 1e30, here and in qsa_prompt_attn.
  */
 int qsa_paged_decode(const qsa_paged_cache* cache, const qsa_batch* batch, int rows, int max_q,
                      int max_len, int dtype, int hq, const void* q, int64_t ldq, const void* gate,
@@ -375,7 +375,9 @@ size_t qsa_prompt_attn_workspace_bytes(int nseq, int rows_q, int rows_k, int hq,
  * and is 0 when it sees none.  q, gate (or NULL), out [rows_q][hq][256] and k, v
  * [rows_k][hkv][256] of QSA_F16 or QSA_BF16 (the tensor cores' types: fp32 rows are refused,
  * fp32 callers cast or use the paged cache).  Rows at or past cu_q[nseq] are left as they were;
- * what lies behind a sequence's keys is not used, whatever it holds.  Few rows against many
+ * what lies behind a sequence's keys is not used, whatever it holds.  A k row reaches only the
+ * rows that see it; the v rows of a sequence are finite (a weight of 0 times a v that is not
+ * is NaN, also for rows that do not see it).  Few rows against many
  * keys are split over the keys and joined through ws (qsa_prompt_attn_workspace_bytes(...) bytes,
  * one call at a time; may be NULL where that is 0).  The result is the same in every run.  Waits
  * are bounded and report through qsa_device_status.

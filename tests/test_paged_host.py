@@ -76,7 +76,7 @@ def test_decode_refuses(lib):
     assert decode(lib, q=P + 2) == ARG
     assert decode(lib, out=None) == ARG
     assert decode(lib, gate=P, ldg=100) == ARG and "gate" in qsa.last_error()
-    for scale in (0.0, -0.0625, float("nan"), float("inf")):
+    for scale in (0.0, -0.0625, float("nan"), float("inf"), 2.0e30):
         assert decode(lib, scale=scale) == ARG and "scale" in qsa.last_error()
         assert prompt(lib, scale=scale) == ARG and "scale" in qsa.last_error()
     assert decode(lib, ws=None) == WORKSPACE

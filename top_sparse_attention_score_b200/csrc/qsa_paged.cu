@@ -90,9 +90,10 @@ cudaError_t launch_read(const qsa::PagedBatch& b, const qsa::PagedCells& c, int 
                     dim3(32 * qsa::kPagedWarps), 0, s, b, c, rows, static_cast<T*>(k), static_cast<T*>(v), ldk, ldv);
 }
 
-// A positive finite softmax scale (the kernels take a tile's largest score before they scale it).
+// A positive softmax scale (the kernels take a tile's largest score before they scale it) that
+// stays finite in log2 units.
 int check_scale(float scale) {
-  if (!(scale > 0.f) || scale > 3.0e38f) return fail(QSA_ERR_ARG, "scale = %g must be positive and finite", scale);
+  if (!(scale > 0.f) || scale > 1.0e30f) return fail(QSA_ERR_ARG, "scale = %g must be positive and at most 1e30", scale);
   return QSA_OK;
 }
 
