@@ -307,7 +307,7 @@ typedef struct qsa_paged_cache {
  *           cu_q[s+1] - 1, its LAST positions: row j of n is position kv_len - n + j.
  *           NULL: one row per sequence.
  * Sequences may be empty (no rows, or no cells).  Packed rows at or past cu_q[nseq] belong to
- * no sequence: they are not read, and outputs there are left as they were.
+ * no sequence: what they hold is not used, and outputs there are left as they were.
  * 1 <= nseq <= QSA_MAX_ROWS, 0 <= rows <= QSA_MAX_PACKED packed rows in the arrays.
  */
 typedef struct qsa_batch {

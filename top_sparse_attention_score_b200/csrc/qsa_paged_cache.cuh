@@ -11,8 +11,8 @@
 // scales out (or back), so HBM bandwidth bounds long calls and latency short ones.  One warp
 // takes a whole packed row (all KV heads, K and V), so the search for the row's sequence and
 // the page lookup are paid once, and its 2 * hkv head rows go through four at a time with
-// all their loads issued first.  A lane holds 8 consecutive values: a group of 32 is four
-// neighbouring lanes (two shuffles for its maximum), and every access is 8 to 16 bytes a lane.
+// all their loads issued first.  A lane of the write holds 8 consecutive values: a group of 32 is
+// four neighbouring lanes (two shuffles for its maximum); every access is 8 to 16 bytes a lane.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -187,13 +187,9 @@ __global__ void __launch_bounds__(32 * kPagedWarps) paged_write_kernel(PagedBatc
   // No early launch of dependents: a dependent may read the cells before its own wait.
   griddep_wait();
   if (r >= rows) return;
-  const int s = batch_find(b, r, lane);
-  if (s < 0) return;
-  const int cell = batch_cell(b, s, batch_position(b, s, r));
-  if (cell < 0) return;
   const int items = 2 * c.hkv;
-  for (int i0 = 0; i0 < items; i0 += 4) {
-    Row8<T> raw[4];
+  Row8<T> raw[4];
+  auto load = [&](int i0) {
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const int i = i0 + u;
@@ -202,6 +198,14 @@ __global__ void __launch_bounds__(32 * kPagedWarps) paged_write_kernel(PagedBatc
         raw[u].load(src + 8 * lane);
       }
     }
+  };
+  load(0);  // on its way while the row's cell is looked up
+  const int s = batch_find(b, r, lane);
+  if (s < 0) return;
+  const int cell = batch_cell(b, s, batch_position(b, s, r));
+  if (cell < 0) return;
+  for (int i0 = 0; i0 < items; i0 += 4) {
+    if (i0 > 0) load(i0);
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const int i = i0 + u;
@@ -234,6 +238,18 @@ __global__ void __launch_bounds__(32 * kPagedWarps) paged_write_kernel(PagedBatc
   }
 }
 
+// The runs of consecutive values that a lane of the read has of a head row: fp32 rows 2 of 4, so that
+// each store of a warp is 512 consecutive bytes (40000 rows of 2 KV heads: 40 us, and 56 with one run of
+// 8 stored as two float4), 16-bit rows 1 of 8.  The write loads fp32 rows as one run of 8, whose
+// halves meet in L1, and has a shuffle less for it (49 us, with two runs 52).
+template <typename T>
+constexpr int kRuns = sizeof(T) == 4 ? 2 : 1;
+// First value of run h, and the group of 32 that it is in.
+template <typename T>
+__device__ __forceinline__ int run_dim(int lane, int h) { return 8 / kRuns<T> * lane + 128 * h; }
+template <typename T>
+__device__ __forceinline__ int run_group(int lane, int h) { return run_dim<T>(lane, h) >> 5; }
+
 // grid: ceil(rows / 4); block: 128.  A row whose position or page does not exist reads as 0.
 template <typename T>
 __global__ void __launch_bounds__(32 * kPagedWarps) paged_read_kernel(PagedBatch b, PagedCells c, int rows,
@@ -249,16 +265,24 @@ __global__ void __launch_bounds__(32 * kPagedWarps) paged_read_kernel(PagedBatch
   const int items = 2 * c.hkv;
   for (int i0 = 0; i0 < items; i0 += 4) {
     uint2 w[4];
-    float sc[4];
+    float sc[4][2];  // of the lane's runs
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const int i = i0 + u;
       w[u] = make_uint2(0u, 0u);
-      sc[u] = 0.f;
+      sc[u][0] = sc[u][1] = 0.f;
       if (i < items && cell >= 0) {
         const size_t row = static_cast<size_t>(cell) * c.hkv + (i < c.hkv ? i : i - c.hkv);
-        w[u] = *reinterpret_cast<const uint2*>((i < c.hkv ? c.k : c.v) + row * kD + 8 * lane);
-        sc[u] = __half2float((i < c.hkv ? c.ks : c.vs)[row * kNG + (lane >> 2)]);
+        const int8_t* codes = (i < c.hkv ? c.k : c.v) + row * kD;
+        const __half* scales = (i < c.hkv ? c.ks : c.vs) + row * kNG;
+        if constexpr (kRuns<T> == 2) {
+          w[u].x = *reinterpret_cast<const uint32_t*>(codes + run_dim<T>(lane, 0));
+          w[u].y = *reinterpret_cast<const uint32_t*>(codes + run_dim<T>(lane, 1));
+        } else {
+          w[u] = *reinterpret_cast<const uint2*>(codes + run_dim<T>(lane, 0));
+        }
+        sc[u][0] = __half2float(scales[run_group<T>(lane, 0)]);
+        sc[u][1] = kRuns<T> == 2 ? __half2float(scales[run_group<T>(lane, 1)]) : sc[u][0];
       }
     }
 #pragma unroll
@@ -269,10 +293,15 @@ __global__ void __launch_bounds__(32 * kPagedWarps) paged_read_kernel(PagedBatch
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const uint32_t word = e < 4 ? w[u].x : w[u].y;
-        x[e] = static_cast<float>(static_cast<int8_t>((word >> (8 * (e & 3))) & 0xffu)) * sc[u];
+        x[e] = static_cast<float>(static_cast<int8_t>((word >> (8 * (e & 3))) & 0xffu)) * sc[u][e >> 2];
       }
       T* dst = i < c.hkv ? k + r * ldk + i * kD : v + r * ldv + (i - c.hkv) * kD;
-      Row8<T>::store(dst + 8 * lane, x);
+      if constexpr (kRuns<T> == 2) {
+        *reinterpret_cast<float4*>(dst + run_dim<T>(lane, 0)) = make_float4(x[0], x[1], x[2], x[3]);
+        *reinterpret_cast<float4*>(dst + run_dim<T>(lane, 1)) = make_float4(x[4], x[5], x[6], x[7]);
+      } else {
+        Row8<T>::store(dst + run_dim<T>(lane, 0), x);
+      }
     }
   }
 }
