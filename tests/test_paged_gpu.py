@@ -331,6 +331,17 @@ def test_decode_many_sequences(gpu):
     check_decode(gpu, c, 4, torch.float16)
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("n,hq", [(1, 4), (3, 24)])
+def test_decode_ragged_with_empty_ones(gpu, dtype, n, hq):
+    """Long sequences between short ones and empty ones, whose CTAs hold pieces and whole units."""
+    r = np.random.RandomState(16)
+    lens = np.where(r.rand(70) < 0.3, 0, np.exp(r.uniform(0, np.log(3000), 70)).astype(int))
+    rows = r.randint(0, n + 1, 70)
+    c = Case(gpu, lens, rows, page=48, hkv=2, seed=17)
+    check_decode(gpu, c, hq, dtype, max_q=n)
+
+
 def test_decode_default_one_row_each_and_max_len(gpu):
     """cu_q None is one row per sequence; the default max_len is the table's extent."""
     qsa = gpu

@@ -120,7 +120,8 @@ DecodePlan plan_decode(int nseq, int hkv, int group, int max_q, int64_t max_len,
   p.ctas_per_sm = p.tc || p.mt > 3 ? 1 : p.mt == 2 ? 3 : 2;
   p.prows = 16 * p.mt;
   p.block_cells = p.tc ? qsa::kTdCells : 16 * p.groups;
-  p.blocks = static_cast<int64_t>(nseq) * hkv * ((max_len + p.block_cells - 1) / p.block_cells);
+  const int open = p.tc ? qsa::kTdOpen : qsa::kPdOpenCells / p.block_cells;  // blocks that a unit counts for on top
+  p.blocks = static_cast<int64_t>(nseq) * hkv * (open + (max_len + p.block_cells - 1) / p.block_cells);
   p.grid = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(p.blocks, static_cast<int64_t>(sms) * p.ctas_per_sm)));
   p.part_o = 0;
   p.part_ml = align_up(p.part_o + static_cast<size_t>(2) * p.grid * p.prows * QSA_D * 4, 256);

@@ -11,11 +11,14 @@
 // token, 12 rows): a cell costs 90 warp instructions, issued at 0.58 a scheduler and cycle, so
 // what bounds it is their latency, not memory.  fp32 (three products for one): 111 us.
 //
-//  * Work is one flat list of blocks (sequence, KV head, 16 C cells) cut into equal contiguous
-//    ranges, one per CTA: ragged lengths balance themselves and a CTA writes one partial per
-//    sequence and head it touches.  Where a range covers a whole (sequence, head) its CTA writes
-//    the final rows itself.  Only the first and the last unit of a range can be partial, so CTA c
-//    has two partial slots: 2c for a unit begun before it, 2c + 1 for one that goes on after it.
+//  * Work is one flat list of units (sequence, KV head), each of blocks of 16 C cells behind a
+//    stretch of positions for what opening it costs (Q, the first cells' way from HBM, the join),
+//    cut into equal contiguous ranges, one per CTA: ragged lengths balance themselves and a CTA
+//    writes one partial per unit it touches.  32 sequences of 50 to 8192 cells: 49 us without
+//    the opening, 37 with 96 cells for it, 35 with 144 or 192 (event times, about 5 us high).
+//    Where a range covers a whole unit its CTA writes the final rows itself.  Only the first and
+//    the last unit of a range can be partial, so CTA c has two partial slots: 2c for a unit begun
+//    before it, 2c + 1 for one that goes on after it.
 //    No counter or atomic orders anything.
 //  * Two warps hold a tile of 16 query rows, 128 dims each; a group of MT such pairs takes a
 //    16-cell block, C groups take blocks in turn and join once per piece through shared memory.
@@ -138,6 +141,7 @@ __device__ __forceinline__ void pd_write8(const PdArgs& a, int row, int head, in
 }
 
 constexpr int kPdW = 2;           // warps of a row tile
+constexpr int kPdOpenCells = 144;  // cells that opening a unit counts for
 constexpr int kPdG = kNG / kPdW;  // scale groups of a warp
 
 template <int MT, int C, int STAGES, bool kSplit>
@@ -177,10 +181,12 @@ __global__ void __launch_bounds__(32 * kPdW * MT * C, MINB) paged_decode_kernel(
   griddep_wait();
 
   // ---- this CTA's range of the flat list, and the unit it starts in (every warp the same)
+  constexpr int kOpen = kPdOpenCells / CB;
+  auto span = [](int blocks) { return blocks > 0 ? kOpen + blocks : 0; };  // a unit's positions of the list
   int total = 0;
   for (int s0 = 0; s0 < a.b.nseq; s0 += 32) {
     const int s = s0 + lane;
-    total += s < a.b.nseq ? (pd_seq(a, s).cells + CB - 1) / CB : 0;
+    total += s < a.b.nseq ? span((pd_seq(a, s).cells + CB - 1) / CB) : 0;
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
@@ -189,10 +195,10 @@ __global__ void __launch_bounds__(32 * kPdW * MT * C, MINB) paged_decode_kernel(
   const int from = min(total, static_cast<int>(blockIdx.x) * per), to = min(total, from + per);
   griddep_launch();  // the join waits for this grid before it reads anything
   if (from >= to) return;
-  int seq = 0, before = 0;  // before: blocks of the sequences in front of `seq`
+  int seq = 0, before = 0;  // before: positions of the sequences in front of `seq`
   for (int s0 = 0, base = 0; s0 < a.b.nseq; s0 += 32) {
     const int s = s0 + lane;
-    const int nb = s < a.b.nseq ? (pd_seq(a, s).cells + CB - 1) / CB * hkv : 0;
+    const int nb = s < a.b.nseq ? span((pd_seq(a, s).cells + CB - 1) / CB) * hkv : 0;
     int inc = nb;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -214,15 +220,16 @@ __global__ void __launch_bounds__(32 * kPdW * MT * C, MINB) paged_decode_kernel(
   PdSeq q = pd_seq(a, seq);
   int nb = (q.cells + CB - 1) / CB;
   while (at < to) {
-    while (at >= before + nb * hkv) {  // sequences without cells have no blocks
-      before += nb * hkv;
+    while (at >= before + span(nb) * hkv) {  // sequences without cells have no positions
+      before += span(nb) * hkv;
       q = pd_seq(a, ++seq);
       nb = (q.cells + CB - 1) / CB;
     }
-    const int kvh = (at - before) / nb;
-    const int u0 = before + kvh * nb;          // the unit's blocks in the flat list
-    const int blk0 = at - u0, blk1 = min(nb, to - u0);
-    at = u0 + blk1;
+    const int kvh = (at - before) / span(nb);
+    const int u0 = before + kvh * span(nb) + kOpen;  // position of the unit's first block
+    const int blk0 = max(at - u0, 0), blk1 = min(nb, to - u0);
+    at = u0 + nb;
+    if (blk1 <= blk0) break;  // the range ends before the unit's first block
     const int unit = seq * hkv + kvh;
     const int first_cta = u0 / per, pieces = (u0 + nb - 1) / per - first_cta + 1;
     if (blk0 == 0 && tid == 0) a.unit[unit] = make_int2(first_cta, pieces);

@@ -31,6 +31,9 @@ namespace qsa {
 constexpr int kTdCells = 64;              // cells of a block
 constexpr int kTdTile = kTdCells * kD * 2;  // 32 KB: a converted K or V block
 constexpr int kTdStages = 2;
+// Blocks that opening a unit counts for in the list.  40 sequences of 50 to 4000 cells, up to 4 rows: 73 us
+// without, 62 with 2, 49 with 5 to 10; 16 of 1000 to 16384: 70 without, 61, 57 (event times, 5 us high).
+constexpr int kTdOpen = 8;
 constexpr int kTdConvWarps = 16;
 // Warpgroups: softmax; MMA and three idle warps; four of conversion.
 constexpr int kTdThreads = 256 + 32 * kTdConvWarps;
@@ -53,19 +56,50 @@ struct __align__(16) TdBarriers {
 };
 constexpr int kTdSmemBytes = 1024 + 2 * kTdStages * kTdTile + static_cast<int>(sizeof(TdBarriers));
 
-// Walks the flat list: block f of it is block `blk` of the unit (seq, kvh).
+// Walks the blocks of the flat list: block `blk` of the unit (seq, kvh).
 struct TdWalk {
-  int seq, before, nb;  // sequence, blocks in front of it, its blocks per KV head
+  int seq, before, nb;  // sequence, positions in front of it (where the walk began), its blocks per KV head
   PdSeq q;
   int kvh, blk;
 };
 
 __device__ __forceinline__ int td_blocks(const PdSeq& q) { return (q.cells + kTdCells - 1) / kTdCells; }
 
-// To block f of the flat list, within the walk's sequence.
-__device__ __forceinline__ void td_open(TdWalk& w, int f) {
-  w.kvh = (f - w.before) / w.nb;
-  w.blk = (f - w.before) - w.kvh * w.nb;
+// Positions of a sequence's unit in the list: what opening it costs, then its blocks.
+__device__ __forceinline__ int td_span(int blocks) { return blocks > 0 ? kTdOpen + blocks : 0; }
+
+// The walk at position f of the list (f below its length), at the unit's first block where f is in
+// front of it.  Returns the number of blocks in front of f.
+__device__ __forceinline__ int td_open(const PdArgs& a, TdWalk& w, int f, int lane) {
+  const int hkv = a.c.hkv;
+  w.seq = w.before = 0;
+  int units = 0;  // with blocks, in front of the sequence
+  for (int s0 = 0, base = 0; s0 < a.b.nseq; s0 += 32) {
+    const int s = s0 + lane;
+    const int np = s < a.b.nseq ? td_span(td_blocks(pd_seq(a, s))) * hkv : 0;
+    int inc = np;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += y;
+    }
+    const uint32_t past = __ballot_sync(0xffffffffu, base + inc > f), some = __ballot_sync(0xffffffffu, np > 0);
+    if (past) {
+      const int l = __ffs(past) - 1;
+      w.seq = s0 + l;
+      w.before = base + __shfl_sync(0xffffffffu, inc - np, l);
+      units += __popc(some & ((1u << l) - 1u)) * hkv;
+      break;
+    }
+    base += __shfl_sync(0xffffffffu, inc, 31);
+    units += __popc(some) * hkv;
+  }
+  w.q = pd_seq(a, w.seq);
+  w.nb = td_blocks(w.q);
+  const int span = td_span(w.nb);
+  w.kvh = (f - w.before) / span;
+  w.blk = max((f - w.before) - w.kvh * span - kTdOpen, 0);
+  return w.before - units * kTdOpen + w.kvh * w.nb + w.blk;
 }
 
 // To the next block of the flat list, which has one; true where it begins a unit.
@@ -117,42 +151,29 @@ __global__ void __launch_bounds__(kTdThreads, 1) paged_decode_tc_kernel(PdArgs a
 
   griddep_wait();
   // ---- this CTA's range of the flat list, and where it starts (every warp the same)
-  int total = 0;
+  int total = 0, total_blocks = 0;
   for (int s0 = 0; s0 < a.b.nseq; s0 += 32) {
     const int s = s0 + lane;
-    total += s < a.b.nseq ? td_blocks(pd_seq(a, s)) : 0;
+    const int nb = s < a.b.nseq ? td_blocks(pd_seq(a, s)) : 0;
+    total += td_span(nb);
+    total_blocks += nb;
   }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  for (int o = 16; o > 0; o >>= 1) {
+    total += __shfl_xor_sync(0xffffffffu, total, o);
+    total_blocks += __shfl_xor_sync(0xffffffffu, total_blocks, o);
+  }
   total *= hkv;
+  total_blocks *= hkv;
   const int per = max(1, (total + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x));
   const int from = min(total, static_cast<int>(blockIdx.x) * per), to = min(total, from + per);
   griddep_launch();  // the join waits for this grid before it reads anything
   if (from >= to) return;
   TdWalk walk;
-  walk.seq = 0;
-  walk.before = 0;
-  for (int s0 = 0, base = 0; s0 < a.b.nseq; s0 += 32) {
-    const int s = s0 + lane;
-    const int nb = s < a.b.nseq ? td_blocks(pd_seq(a, s)) * hkv : 0;
-    int inc = nb;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += y;
-    }
-    const uint32_t past = __ballot_sync(0xffffffffu, base + inc > from);
-    if (past) {
-      const int l = __ffs(past) - 1;
-      walk.seq = s0 + l;
-      walk.before = base + __shfl_sync(0xffffffffu, inc - nb, l);
-      break;
-    }
-    base += __shfl_sync(0xffffffffu, inc, 31);
-  }
-  walk.q = pd_seq(a, walk.seq);
-  walk.nb = td_blocks(walk.q);
-  td_open(walk, from);
+  int nblocks = total_blocks;  // of this CTA
+  if (to < total) nblocks = td_open(a, walk, to, lane);
+  nblocks -= td_open(a, walk, from, lane);
+  if (nblocks <= 0) return;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kTdStages; ++i) {
@@ -179,7 +200,6 @@ __global__ void __launch_bounds__(kTdThreads, 1) paged_decode_tc_kernel(PdArgs a
   tc_fence_after();
   const uint32_t tmem = tb.tmem_base;
   const uint32_t tmem_q = tmem + 2 * kTdCells, tmem_o = tmem + 256;
-  const int nblocks = to - from;
 
   if (warp >= 8) {
     regs_shrink<kTdRegsConv>();
@@ -381,10 +401,10 @@ __global__ void __launch_bounds__(kTdThreads, 1) paged_decode_tc_kernel(PdArgs a
       if (lane == 0) mbar_arrive(&tb.q_ready);
     };
     put_q();
+    int u0 = walk.before + walk.kvh * td_span(walk.nb) + kTdOpen;  // position of the unit's first block
     for (int piece = 0; i < nblocks; ++piece) {
       const PdSeq q = walk.q;
       const int kvh = walk.kvh, unit = walk.seq * hkv + kvh, nb = walk.nb;
-      const int u0 = from + i - walk.blk;  // the unit's first block in the flat list
       const int blk0 = walk.blk, blk1 = min(nb, to - u0);
       const int first_cta = u0 / per, pieces = (u0 + nb - 1) / per - first_cta + 1;
       if (blk0 == 0 && threadIdx.x == 0) a.unit[unit] = make_int2(first_cta, pieces);
@@ -459,6 +479,7 @@ __global__ void __launch_bounds__(kTdThreads, 1) paged_decode_tc_kernel(PdArgs a
         __syncwarp();
         if (lane == 0) mbar_arrive(&tb.p_ready[i & 1]);
       }
+      u0 += nb + kTdOpen;  // of the next one
       // the next piece's Q: the scores of this one's last block are complete
       if (i < nblocks) {
         walk.blk = blk1 - 1;
